@@ -23,6 +23,8 @@ __all__ = [
     "qmm_moe_swiglu", "qmm_gemv_residual", "qmm_moe_combine", "qmm_gemm_grouped",
     "qmm_gemm_grouped_workspace_bytes", "qmm_gemm_noalloc", "qmm_set_override", "overrides",
     "QMM_NOALLOC_SCRATCH_BYTES",
+    "KvCache", "qmm_norm_residual", "qmm_kv_append", "qmm_attn_cache", "qmm_attn_cache_workspace_bytes",
+    "qmm_attn_prompt",
     "qmm_get_plan", "qmm_status_string", "qmm_last_error", "qmm_abi_version",
     "QMM_OK", "QMM_ERR_INVALID_ARGUMENT", "QMM_ERR_UNSUPPORTED", "QMM_ERR_MISALIGNED",
     "QMM_ERR_DEVICE", "EXPORTED_SYMBOLS",
@@ -40,6 +42,7 @@ EXPORTED_SYMBOLS = (
     "qmm_gemv_batch_prepare", "qmm_gemv_batched", "qmm_gemv_swiglu", "qmm_gemm_f16out",
     "qmm_moe_swiglu", "qmm_gemv_residual", "qmm_moe_combine", "qmm_gemm_grouped",
     "qmm_gemm_grouped_workspace_bytes", "qmm_gemm_noalloc", "qmm_set_override",
+    "qmm_norm_residual", "qmm_kv_append", "qmm_attn_cache", "qmm_attn_cache_workspace_bytes", "qmm_attn_prompt",
     "qmm_get_plan", "qmm_status_string", "qmm_last_error", "qmm_abi_version",
 )
 
@@ -101,6 +104,35 @@ class GemmMember(ctypes.Structure):
 assert ctypes.sizeof(GemmMember) == 40
 
 
+class KvCache(ctypes.Structure):
+    """qmm_kv_cache: a paged key/value cache (device tensors or addresses; the
+    tensors have to outlive it and are kept alive by it)."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("k_mins", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("v_mins", ctypes.c_void_p),
+        ("pages", ctypes.c_int64),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("bits", ctypes.c_int32),
+        ("group_size", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+    def __init__(self, k, k_scales, k_mins, v, v_scales, v_mins, pages, kv_heads, head_dim, page_size, bits,
+                 group_size):
+        super().__init__(_addr(k), _addr(k_scales), _addr(k_mins), _addr(v), _addr(v_scales), _addr(v_mins),
+                         int(pages), int(kv_heads), int(head_dim), int(page_size), int(bits), int(group_size), 0)
+        self.keep = (k, k_scales, k_mins, v, v_scales, v_mins)
+
+
+assert ctypes.sizeof(KvCache) == 80
+
+
 def library_path() -> str:
     """In-tree libqmm.so, or the file named by $QMM_LIBRARY (tuning builds)."""
     return os.environ.get("QMM_LIBRARY") or os.path.join(_HERE, _LIB_NAME)
@@ -140,11 +172,18 @@ def load():
     lib.qmm_unpack.argtypes = [p, p, i64, i64, ci, p]
     lib.qmm_gemv_batch_prepare.argtypes = [p, i64, ci, ci]
     lib.qmm_gemv_batched.argtypes = [p, p, i64, ci, ci, p]
+    cf, pc = ctypes.c_float, ctypes.POINTER(KvCache)
+    lib.qmm_norm_residual.argtypes = [p, ci, i64, p, p, i64, cf, p, p, p, p, i64, i64, cf, p]
+    lib.qmm_kv_append.argtypes = [pc, p, p, p, ci, i64, i64, i64, p, p, cf, p, ci, ci, p, p, p, p, p, ci, i64, ci, p]
+    lib.qmm_attn_cache.argtypes = [pc, p, p, i64, p, i64, p, i64, ci, ci, cf, p, sz, p]
+    lib.qmm_attn_cache_workspace_bytes.argtypes = [pc, i64, ci, ci, i64]
+    lib.qmm_attn_cache_workspace_bytes.restype = sz
+    lib.qmm_attn_prompt.argtypes = [p, p, p, p, p, i64, i64, ci, ci, ci, i64, i64, i64, i64, cf, p]
     lib.qmm_get_plan.argtypes = [ci, i64, i64, i64, ci, ci, ci, sz, ctypes.POINTER(_Plan)]
     for f in ("qmm_gemv", "qmm_gemm", "qmm_moe_gemm", "qmm_unpack", "qmm_get_plan",
               "qmm_gemv_batch_prepare", "qmm_gemv_batched", "qmm_gemv_swiglu", "qmm_gemm_f16out", "qmm_moe_swiglu",
               "qmm_gemv_residual", "qmm_moe_combine", "qmm_gemm_grouped", "qmm_gemm_noalloc",
-              "qmm_set_override"):
+              "qmm_set_override", "qmm_norm_residual", "qmm_kv_append", "qmm_attn_cache", "qmm_attn_prompt"):
         getattr(lib, f).restype = ci
     lib.qmm_status_string.argtypes = [ci]
     lib.qmm_status_string.restype = ctypes.c_char_p
@@ -322,6 +361,48 @@ def qmm_moe_swiglu(gate_w, gate_scales, gate_mins, up_w, up_scales, up_mins, x, 
                                  int(n_experts), int(n), int(k), int(bits), int(group_size),
                                  _stream(stream)),
            "qmm_moe_swiglu")
+
+
+def qmm_norm_residual(y, y_fp16, y_stride, post_weight, gate, gate_stride, scale, residual, h, pre_weight, x, rows, n,
+                      eps, stream=None) -> None:
+    """h = residual + scale * gate * rmsnorm(y); x = fp16(rmsnorm(h)); asynchronous."""
+    _check(load().qmm_norm_residual(_addr(y), bool(y_fp16), int(y_stride), _addr(post_weight), _addr(gate),
+                                    int(gate_stride), float(scale), _addr(residual), _addr(h), _addr(pre_weight),
+                                    _addr(x), int(rows), int(n), float(eps), _stream(stream)),
+           "qmm_norm_residual")
+
+
+def qmm_kv_append(cache, q, k, v, in_fp16, q_stride, k_stride, v_stride, q_norm, k_norm, eps, inv_freq, rot_dim,
+                  interleaved, positions, slots, q_out, k_out, v_out, out_cached, tokens, q_heads, stream=None) -> None:
+    """Rotated queries, and keys and values into the cache's slots (``cache``: a ``KvCache``); asynchronous."""
+    _check(load().qmm_kv_append(cache, _addr(q), _addr(k), _addr(v), bool(in_fp16), int(q_stride), int(k_stride),
+                                int(v_stride), _addr(q_norm), _addr(k_norm), float(eps), _addr(inv_freq),
+                                int(rot_dim), bool(interleaved), _addr(positions), _addr(slots), _addr(q_out),
+                                _addr(k_out), _addr(v_out), bool(out_cached), int(tokens), int(q_heads),
+                                _stream(stream)),
+           "qmm_kv_append")
+
+
+def qmm_attn_cache(cache, q, page_table, table_stride, kv_lens, max_kv_len, out, n_seqs, q_len, q_heads, scale,
+                   workspace=None, workspace_bytes=0, stream=None) -> None:
+    """Attention of each sequence's newest ``q_len`` tokens over its cached rows; asynchronous."""
+    _check(load().qmm_attn_cache(cache, _addr(q), _addr(page_table), int(table_stride), _addr(kv_lens),
+                                 int(max_kv_len), _addr(out), int(n_seqs), int(q_len), int(q_heads), float(scale),
+                                 _addr(workspace), int(workspace_bytes), _stream(stream)),
+           "qmm_attn_cache")
+
+
+def qmm_attn_cache_workspace_bytes(cache, n_seqs, q_len, q_heads, max_kv_len) -> int:
+    return int(load().qmm_attn_cache_workspace_bytes(cache, int(n_seqs), int(q_len), int(q_heads), int(max_kv_len)))
+
+
+def qmm_attn_prompt(q, k, v, seq_offsets, out, tokens, n_seqs, q_heads, kv_heads, head_dim, q_stride, k_stride,
+                    v_stride, out_stride, scale, stream=None) -> None:
+    """Causal attention in each of the packed sequences; asynchronous."""
+    _check(load().qmm_attn_prompt(_addr(q), _addr(k), _addr(v), _addr(seq_offsets), _addr(out), int(tokens),
+                                  int(n_seqs), int(q_heads), int(kv_heads), int(head_dim), int(q_stride),
+                                  int(k_stride), int(v_stride), int(out_stride), float(scale), _stream(stream)),
+           "qmm_attn_prompt")
 
 
 def qmm_unpack(w_packed, codes, n, k, bits, stream=None) -> None:

@@ -15,7 +15,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqmm.so")
 # (source, extra defines, object name); gemv_bits.hip is built once per width.
 SOURCES = [("qmm_api.hip", [], "qmm_api.o"), ("gemm.hip", [], "gemm.o"), ("gemm_wl.hip", [], "gemm_wl.o"),
-           ("unpack.hip", [], "unpack.o")] + [
+           ("unpack.hip", [], "unpack.o"), ("layer_api.hip", [], "layer_api.o"), ("norm.hip", [], "norm.o"),
+           ("kv_append.hip", [], "kv_append.o"), ("attn_cache.hip", [], "attn_cache.o"),
+           ("attn_prompt.hip", [], "attn_prompt.o")] + [
     ("gemv_bits.hip", ["-DQMM_BITS=%d" % b], "gemv_b%d.o" % b) for b in (2, 3, 4, 5, 6, 8, 16)]
 ARCH = os.environ.get("QMM_OFFLOAD_ARCH", "gfx950")
 

@@ -18,6 +18,7 @@
 #include <mutex>
 
 #include "../../include/qmm.h"
+#include "layer_kernels.h"
 #include "qmm_kernels.h"
 
 using namespace qmm;
@@ -63,6 +64,22 @@ qmm_status ok() {
     g_err[0] = '\0';
     return QMM_OK;
 }
+
+}  // namespace
+
+namespace qmm {
+// The same for the entry points of layer_api.hip (QMM_OK clears the text).
+qmm_status report(qmm_status st, const char* fmt, ...) {
+    if (st == QMM_OK) return ok();
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return st;
+}
+}  // namespace qmm
+
+namespace {
 
 bool bits_supported(int bits) {
     return bits == 2 || bits == 3 || bits == 4 || bits == 5 || bits == 6 || bits == 8 || bits == 16;

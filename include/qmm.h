@@ -333,6 +333,135 @@ QMM_API qmm_status qmm_moe_combine(const void *w_packed, const void *scales, con
                                    int64_t p_rows, int64_t n_experts, int64_t n, int64_t k,
                                    int bits, int group_size, void *stream);
 
+/* ---- The attention half of a decoder layer -----------------------------
+ * What stands between a layer's products: qmm_norm_residual turns one
+ * product's fp32 (or fp16) output into the residual stream and the fp16 input
+ * of the next, qmm_kv_append takes the q, k and v products to rotated queries
+ * and a paged cache, qmm_attn_prompt and qmm_attn_cache give the input of the
+ * output projection.  The rules at the top of this file hold (host checks,
+ * no allocation, asynchronous on `stream`, errors); results repeat bit for
+ * bit for the same arguments and plan.
+ *
+ * Norm, gate and residual around a block, per row r of n elements:
+ *   u = y[r]                                     (y fp32, or fp16 with y_fp16)
+ *   u = u * rsqrt(mean(u^2) + eps) * post_weight (post_weight not NULL)
+ *   u = u * gate[r]                              (gate not NULL)
+ *   h[r] = residual[r] + scale * u               (residual NULL: scale * u)
+ *   x[r] = fp16(h[r] * rsqrt(mean(h[r]^2) + eps) * pre_weight)
+ *   y  [rows] rows y_stride elements apart; NULL: h is residual, nothing is
+ *      written to the argument h (it may be NULL), and residual is required.
+ *   post_weight, pre_weight fp32 [n] or NULL (no norm on y; weight one on x).
+ *   gate fp32, rows gate_stride elements apart; 0: one row for all.
+ *   residual, h fp32 [rows][n]; h may be residual itself, or NULL (not kept).
+ *   x fp16 [rows][n] or NULL (not wanted).  h or x has to be given.
+ * Sums are fp32 in a fixed order.  n at most 32768, rows below 2^22, else
+ * QMM_ERR_UNSUPPORTED.  Pointers aligned to their elements; 16-byte aligned
+ * rows (n and strides multiples of 4) are faster.  x must not overlap an
+ * input; neither must h, but for residual.                                 */
+QMM_API qmm_status qmm_norm_residual(const void *y, int y_fp16, int64_t y_stride,
+                                     const float *post_weight, const float *gate,
+                                     int64_t gate_stride, float scale, const float *residual,
+                                     float *h, const float *pre_weight, void *x, int64_t rows,
+                                     int64_t n, float eps, void *stream);
+
+/* A paged key/value cache (host struct of device pointers; the caller owns
+ * the memory).  Page p, kv head j and place i hold one row of head_dim values:
+ *   k, v          [pages][kv_heads][page_size] rows of head_dim codes, the
+ *                 row bitstream of the weights (head_dim * bits / 32 words);
+ *                 bits 16: fp16 values
+ *   *_scales, *_mins  fp16 [pages][kv_heads][head_dim / group_size][page_size]:
+ *                 the row's value d is scale * code + min of its group
+ *                 d / group_size.  NULL at bits 16.
+ * A slot is page * page_size + place.
+ * bits 4, 8 or 16 (2, 3, 5, 6: QMM_ERR_UNSUPPORTED); head_dim 64 or 128 (other
+ * positive: QMM_ERR_UNSUPPORTED); group_size a multiple of 32 that divides
+ * head_dim (not looked at with 16 bits); page_size a power of two from 16 to
+ * 65536 (other positive: QMM_ERR_UNSUPPORTED); kv_heads 1 to 4096.  Arrays
+ * 16-byte aligned.  Any size: rows are addressed with 64-bit offsets.      */
+typedef struct qmm_kv_cache {
+    void *k, *k_scales, *k_mins;
+    void *v, *v_scales, *v_mins;
+    int64_t pages;
+    int32_t kv_heads, head_dim, page_size, bits, group_size, reserved;
+} qmm_kv_cache;
+
+/* New tokens' q, k and v rows (fp32, or fp16 with in_fp16; token rows
+ * *_stride elements apart, so one fused product serves as well as three):
+ *   q, k: optional per-head norm, x * rsqrt(mean(x^2) + eps) * weight (q_norm,
+ *     k_norm fp32 [head_dim] or NULL), then the rotation of the first rot_dim
+ *     elements by position: with t = positions[token] * inv_freq[i], elements
+ *     (a, b) = (x[i], x[i + rot_dim / 2]), or (x[2i], x[2i + 1]) if
+ *     interleaved, become (a cos t - b sin t, b cos t + a sin t).  The angle is
+ *     formed in 64 bits.
+ *   q_out fp16 [tokens][q_heads][head_dim]
+ *   k, v: into slot slots[token] of the cache.  Per group: min fp16(lowest),
+ *     scale fp16((highest - lowest) / (2^bits - 1)), code
+ *     round((x - min) / scale) within 0 .. 2^bits - 1 (0 where the scale is 0).
+ *   k_out, v_out fp16 [tokens][kv_heads][head_dim] or NULL: what prompt
+ *     attention reads; with out_cached the values that the cache stands for
+ *     (fp16(scale * code + min)), else the rows before quantization.
+ *   positions int32 [tokens], slots int64 [tokens] (device).  A slot outside
+ *     [0, pages * page_size) (-1 for padding) is not stored.  slots NULL:
+ *     nothing is stored and the cache's arrays are not looked at.  The slots of
+ *     one call have to differ: one that is given twice holds a mixture of both.
+ *   inv_freq fp32 [rot_dim / 2]; rot_dim 0 (no rotation, positions and
+ *     inv_freq may be NULL) to head_dim, a multiple of 16.
+ * q_heads 0 (q and q_out may be NULL) to 4096; rows 16-byte aligned (pointers
+ * and strides); tokens below 2^24.  A value that is not finite, or beyond
+ * fp16, makes its group's scale or min so: the group reads back as NaN.     */
+QMM_API qmm_status qmm_kv_append(const qmm_kv_cache *cache /* host */, const void *q,
+                                 const void *k, const void *v, int in_fp16, int64_t q_stride,
+                                 int64_t k_stride, int64_t v_stride, const float *q_norm,
+                                 const float *k_norm, float eps, const float *inv_freq,
+                                 int rot_dim, int interleaved, const int32_t *positions,
+                                 const int64_t *slots, void *q_out, void *k_out, void *v_out,
+                                 int out_cached, int64_t tokens, int q_heads, void *stream);
+
+/* Attention of the newest q_len tokens of n_seqs sequences over the cache.
+ *   q, out fp16 [n_seqs][q_len][q_heads][head_dim], 16-byte aligned; query
+ *     head j reads kv head j / (q_heads / kv_heads).
+ *   page_table int32 [n_seqs] rows of table_stride entries (device): cached
+ *     row t of sequence i is place t % page_size of page
+ *     page_table[i][t / page_size].  Entries behind a sequence's last page are
+ *     not read.  An entry outside [0, pages) makes the sequence's rows NaN.
+ *   kv_lens int32 [n_seqs] (device): cached rows of a sequence, the q_len new
+ *     ones included; values outside [0, max_kv_len] are clamped.
+ *   Token i of q_len sees rows t < kv_len - q_len + 1 + i; one that sees no
+ *     row gets zeros.  Rows behind kv_len may hold anything.  A value that is
+ *     not finite reaches the tokens that see it and no others.
+ *   max_kv_len (host): at most table_stride * page_size and below 2^30.
+ *   scale multiplies the scores (before the softmax).
+ *   workspace: device scratch, 16-byte aligned, for partial sums; its contents
+ *     are not looked at.  With less than qmm_attn_cache_workspace_bytes() long
+ *     sequences are split less, with none not at all.  Calls that overlap need
+ *     a workspace each.
+ * q_len 1 to 256.                                                           */
+QMM_API qmm_status qmm_attn_cache(const qmm_kv_cache *cache /* host */, const void *q,
+                                  const int32_t *page_table, int64_t table_stride,
+                                  const int32_t *kv_lens, int64_t max_kv_len, void *out,
+                                  int64_t n_seqs, int q_len, int q_heads, float scale,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+QMM_API size_t qmm_attn_cache_workspace_bytes(const qmm_kv_cache *cache /* host */,
+                                              int64_t n_seqs, int q_len, int q_heads,
+                                              int64_t max_kv_len);
+
+/* Causal attention over whole prompts packed behind each other.
+ *   q, out fp16 [tokens] rows of [q_heads][head_dim], k, v fp16 [tokens] rows of
+ *     [kv_heads][head_dim]; rows *_stride elements apart, 16-byte aligned
+ *     (pointers and strides).  out must not overlap an input.
+ *   seq_offsets int32 [n_seqs + 1] (device), non-decreasing: sequence i is
+ *     rows seq_offsets[i] .. seq_offsets[i + 1] - 1, and row r of it sees rows
+ *     seq_offsets[i] .. r.  Rows that no sequence covers are left as they were.
+ *     Whatever the offsets hold, nothing outside the given rows is touched.
+ *   A value that is not finite reaches the rows that see it and no others.
+ * head_dim 64 or 128; q_heads a multiple of kv_heads.  Probabilities are
+ * rounded to fp16 for the second product; sums are fp32.                    */
+QMM_API qmm_status qmm_attn_prompt(const void *q, const void *k, const void *v,
+                                   const int32_t *seq_offsets, void *out, int64_t tokens,
+                                   int64_t n_seqs, int q_heads, int kv_heads, int head_dim,
+                                   int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                   int64_t out_stride, float scale, void *stream);
+
 /* Codes as bytes: codes[n][k] = q[n][k] (uint8).  Bit-exact view of the
  * packed format, used to check the GPU's bit extraction.                   */
 QMM_API qmm_status qmm_unpack(const void *w_packed, uint8_t *codes, int64_t n, int64_t k,
