@@ -18,8 +18,6 @@ import random
 import torch
 
 own = False
-if own:
-    import gemm_qmm_gemv_amd as qmm
 
 DEV = "cuda"
 EPS = 1e-6
@@ -211,9 +209,13 @@ def prepare(case, seed):
         s["v"] = normal(tokens, hkv, d, dtype=torch.float16)
         s["out"] = torch.zeros((tokens, hq, d), device=DEV, dtype=torch.float16)
     if own and op in ("append", "cache"):
+        import gemm_qmm_gemv_amd as qmm
+
         c = s["cache"]
         s["handle"] = qmm.KvCache(c["k"], c["ks"], c["km"], c["v"], c["vs"], c["vm"], c["k"].shape[0], hkv, d, case["page"], case["bits"], case["group"])
     if own and op == "cache":
+        import gemm_qmm_gemv_amd as qmm
+
         need = qmm.qmm_attn_cache_workspace_bytes(s["handle"], len(lens), q_len, hq, s["max_len"])
         s["workspace"] = torch.zeros(max(need, 16), dtype=torch.uint8, device=DEV)
     return s
@@ -223,6 +225,8 @@ def prepare(case, seed):
 
 
 def _own(s):
+    import gemm_qmm_gemv_amd as qmm
+
     case = s["case"]
     op = case["op"]
     if op == "norm":
