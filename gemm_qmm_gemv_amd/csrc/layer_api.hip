@@ -311,6 +311,8 @@ qmm_status qmm_attn_prompt(const void* q, const void* k, const void* v, const in
     if ((st = check_rows("k", k, k_stride, (int64_t)kv_heads * head_dim, 2)) != QMM_OK) return st;
     if ((st = check_rows("v", v, v_stride, (int64_t)kv_heads * head_dim, 2)) != QMM_OK) return st;
     if ((st = check_rows("out", out, out_stride, (int64_t)q_heads * head_dim, 2)) != QMM_OK) return st;
+    // The kernel addresses 64 rows of k and v at a time with 32-bit offsets.
+    CHECK(k_stride < (1 << 23) && v_stride < (1 << 23), QMM_ERR_UNSUPPORTED, "k or v stride of 2^23 elements or more");
     CHECK(seq_offsets, QMM_ERR_INVALID_ARGUMENT, "NULL seq_offsets");
     CHECK(aligned(seq_offsets, 4), QMM_ERR_MISALIGNED, "seq_offsets not 4-byte aligned");
     int cus = 0;

@@ -454,7 +454,8 @@ QMM_API size_t qmm_attn_cache_workspace_bytes(const qmm_kv_cache *cache /* host 
  *     seq_offsets[i] .. r.  Rows that no sequence covers are left as they were.
  *     Whatever the offsets hold, nothing outside the given rows is touched.
  *   A value that is not finite reaches the rows that see it and no others.
- * head_dim 64 or 128; q_heads a multiple of kv_heads.  Probabilities are
+ * head_dim 64 or 128; q_heads a multiple of kv_heads; k and v strides below
+ * 2^23 (else QMM_ERR_UNSUPPORTED).  Probabilities are
  * rounded to fp16 for the second product; sums are fp32.                    */
 QMM_API qmm_status qmm_attn_prompt(const void *q, const void *k, const void *v,
                                    const int32_t *seq_offsets, void *out, int64_t tokens,
