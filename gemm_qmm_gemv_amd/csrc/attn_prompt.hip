@@ -4,28 +4,35 @@
 //   O[i] = sum_j exp(S[i][j] - max_j S[i][j]) V[j] / sum_j exp(S[i][j] - max_j S[i][j]),
 //   S[i][j] = scale * Q[i] . K[j],  j from the start of i's sequence to i.
 //
-// Bound by the matrix cores.  A work-group holds 128 packed rows of one query
-// head (32 per wave) and walks over the rows' keys in tiles of 64, with a
-// running maximum and sum.  Rows are cut by their place in the packing and
-// not by sequence: a tile of rows may hold the end of one sequence and several
-// short ones, which costs masked work at the borders only and needs no list
-// of tiles.
+// Bound by the matrix cores, the vector units (exponentials) and LDS, which
+// have about the same load.  Short steps on many waves keep all three busy
+// best: a wave holds 32 query rows of one head and takes 32 keys a step, and
+// three (head size 128) or four waves on each SIMD are at different places of
+// it.  8192 tokens, 32 query and 4 key heads of 128: 564 us, 975 TFLOP/s, 83 %
+// of what a large fp16 matrix product of the library reaches on the card (1178;
+// the clock drops to 1.9 GHz under either).  Tried and slower there: two waves
+// per SIMD with the next step's scores formed early (593 us), the same with
+// matrix and vector instructions interleaved by hand (631), 64 rows per wave
+// (829), K and V staged through registers (645).
+//
+// Query rows are cut by their place in the packing and not by sequence: a tile
+// of rows may hold the end of one sequence and several short ones, which costs
+// masked work at the borders only and needs no list of tiles.
 //
 // The products are transposed so that no value changes lanes between them:
 //   S^T = K Q^T puts, in lane l, scores of query row l % 32 at sixteen of 32
 //   keys; O^T = V^T P^T takes them as its right operand as they are, with V^T
 //   read in the same order of keys.  A query row's maximum and sum need one
 //   exchange with lane l ^ 32.
-#include <type_traits>
-
 #include "layer_kernels.h"
 #include "qmm_device.h"
 
 namespace qmm {
 namespace {
 
-constexpr int BN = 64;   // keys per step
 constexpr float NEG_INF = -__builtin_huge_valf();
+// s_waitcnt: all vector memory done (expcnt and lgkmcnt not waited on).
+constexpr int WAIT_LOADS = 0x0F70;
 
 typedef f16 f16x4v __attribute__((ext_vector_type(4)));
 
@@ -92,36 +99,59 @@ __device__ __forceinline__ float halves_max(float v) {
     return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
 }
 
-// Elements from one row of a tile to the next in LDS.  One access to K reads
-// the same 16 bytes of 32 rows, one to V 32 bytes each of four rows: rows
-// start 16 bytes (K) and 64 bytes (V) further into the 256 bytes of banks, so
-// what an access touches at a time lies on different banks, and every address
-// of a lane is one register plus a constant.
-template <int D> constexpr int K_ROW = D + 8;
-template <int D> constexpr int V_ROW = D + 32;
+// 16 bytes per lane from memory to LDS without passing through registers: lane
+// i's land at `to` + 16 i.  An instruction of its own text, because the
+// compiler waits for all loads before any later LDS read if it knows that
+// this one writes LDS; here readers do, before the barrier they share.  m0
+// holds the LDS address and needs one instruction between its write and its
+// use.  There is no register for the load to write, and the address registers
+// are read when it is issued.
+__device__ __forceinline__ void load_to_lds(u32x4 rsrc, u32 offset, u32 to) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :
+                 : "v"(offset), "s"(rsrc), "s"(to)
+                 : "memory");
+}
+__device__ __forceinline__ u32 lds_address(const void* p) {
+    return (u32)(size_t)(const __attribute__((address_space(3))) char*)p;
+}
+// Buffer descriptor of everything from p on (offsets are clamped by the caller).
+__device__ __forceinline__ u32x4 open_rsrc(const void* p) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    return u32x4{(u32)uniform((int)a), (u32)uniform((int)(a >> 32)) & 0xffffu, 0xffffffffu, (u32)RSRC_WORD3};
+}
 
-// RW waves hold 32 query rows each; with KW = 2 two waves share the rows, each
-// taking one half of every tile's keys, and join at the end.
-template <int D, int RW, int KW>
-__global__ void __launch_bounds__(64 * RW * KW, 2) attn_prompt_kernel(PromptArgs a) {
+// A tile of K or V lies in LDS row behind row, as the direct loads put it; the
+// 16-byte chunk c of row r is at place c ^ swizzle(r) of its row.  One access
+// to K reads the same chunk of 32 rows, one to V 32 bytes each of four rows:
+// the exclusive or puts what an access touches at a time on different banks.
+template <int D>
+__device__ __forceinline__ int k_swizzle(int r) { return D == 128 ? r & 15 : r >> 1 & 7; }
+template <int D>
+__device__ __forceinline__ int v_swizzle(int r) { return D == 128 ? (r & 3) << 2 : (r >> 1 & 1) << 2; }
+
+// RW waves hold 32 query rows each; KW of them share the rows, each taking 32 of
+// every 32 KW keys, and join at the end.
+template <int D, int RW, int KW, int BN>
+__global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_kernel(PromptArgs a) {
     constexpr int BM = RW * 32, T = 64 * RW * KW;
-    constexpr int CH = BN * D / 8 / T;     // 16-byte chunks of a tile of K (or of V) per thread
-    constexpr int ROWS = T / (D / 8);      // rows that the work-group's chunks of one round cover
-    constexpr int KBUF = BN * K_ROW<D>, VBUF = BN * V_ROW<D>;
-    __shared__ __align__(16) f16 lds[2 * KBUF + 2 * VBUF];
+    constexpr int CR = D / 8;                // 16-byte chunks of a row
+    constexpr int LROWS = 64 / CR;           // rows that one load of a wave covers
+    constexpr int LOADS = BN * CR / T;       // loads of a tile of K (or of V) per wave
+    constexpr int BUF = BN * D;
+    __shared__ __align__(1024) f16 lds[4 * BUF];
     __shared__ int lds_bad[2][BN], lds_any[2];
     __shared__ int lds_lo[RW], lds_hi[RW], lds_late[RW];
     f16* const lds_k = lds;
-    f16* const lds_v = lds + 2 * KBUF;
+    f16* const lds_v = lds + 2 * BUF;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int rw = wave % RW, kw = wave / RW;
     const int h = lane >> 5, l32 = lane & 31;
-    // Query heads of one key head lie kv_heads work-groups apart: with eight
-    // or a divisor of eight of them, one die (work-groups go round the eight)
-    // reads few key heads.  Later rows see more keys: they start first.
-    const int pos = blockIdx.x % a.q_heads;
-    const int kvh = pos % a.kv_heads, head = kvh * (a.q_heads / a.kv_heads) + pos / a.kv_heads;
-    const int tile = (int)gridDim.x / a.q_heads - 1 - blockIdx.x / a.q_heads;
+    // Grid: kv heads, query heads of each, tiles of rows.  Work-groups go
+    // round the eight dies, so with eight kv heads, or a divisor of eight,
+    // one die reads few of them.  Later rows see more keys: they start first.
+    const int kvh = blockIdx.x, head = kvh * (int)gridDim.y + blockIdx.y;
+    const int tile = (int)(gridDim.z - 1 - blockIdx.z);
     const int row0 = tile * BM, wrow0 = row0 + rw * 32;
     const int row = wrow0 + l32;
 
@@ -150,15 +180,13 @@ __global__ void __launch_bounds__(64 * RW * KW, 2) attn_prompt_kernel(PromptArgs
         sequence_starts<1>(a.offsets, (int)a.n_seqs, a.tokens, rows, starts);
         start = starts[0];
     }
-    int lo = start < 0 ? 0x7fffffff : start, hi = start < 0 ? -1 : row, late = start < 0 ? 0 : start;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const int x = __shfl_xor(lo, o, 64), y = __shfl_xor(hi, o, 64), z = __shfl_xor(late, o, 64);
-        lo = x < lo ? x : lo;
-        hi = y > hi ? y : hi;
-        late = z > late ? z : late;
-    }
-    const int wlo = uniform(lo), whi = uniform(hi), wlate = uniform(late);
+    // (Starts do not decrease from row to row in a packing, so the first and
+    // last row that a sequence covers hold them.)
+    const u32 covered = (u32)__ballot(start >= 0);
+    const int from = covered ? __builtin_ctz(covered) : 0, to = covered ? 31 - __builtin_clz(covered) : 0;
+    const int wlo = covered ? __builtin_amdgcn_readlane(start, from) : 0x7fffffff;
+    const int wlate = covered ? __builtin_amdgcn_readlane(start, to) : 0;
+    const int whi = covered ? wrow0 + to : -1;
     if (lane == 0) {
         lds_lo[rw] = wlo;
         lds_hi[rw] = whi;
@@ -187,67 +215,63 @@ __global__ void __launch_bounds__(64 * RW * KW, 2) attn_prompt_kernel(PromptArgs
     const f16* vp = static_cast<const f16*>(a.v) + kvh * D;
     const int tiles = (bhi - blo) / BN + 1;
 
-    // The thread's chunks of a tile: rows sr, sr + ROWS, ...  Rows past the
-    // last key read as zero: they lie behind the end of the buffer resource
-    // (the offset is all in the vector operand, which the bound is checked
-    // against).
-    const int sr = tid / (D / 8), scol = tid % (D / 8) * 8;
-    auto load_tile = [&](const f16* base, int64_t stride, int j, u32x4 (&w)[CH]) {
-        const int t0 = blo + j * BN;
-        const int left = bhi + 1 - t0 < BN ? bhi + 1 - t0 : BN;
-        const rsrc_t rs = make_rsrc(base + (int64_t)t0 * stride, (uint32_t)(left * (int)stride * 2));
+    // Tile j of K and V goes from memory to buffer b of LDS without passing
+    // through registers.  Rows behind the last key repeat it; they are masked.
+    auto fetch = [&](int j, int b) {
+        const int t0 = blo + j * BN, last = bhi - t0;
+        const u32x4 kr = open_rsrc(kp + (int64_t)t0 * a.k_stride), vr = open_rsrc(vp + (int64_t)t0 * a.v_stride);
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            w[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, ((sr + i * ROWS) * (int)stride + scol) * 2, 0, 0);
+        for (int i = 0; i < LOADS; ++i) {
+            const int r0 = (i * (T / 64) + wave) * LROWS, r = r0 + lane / CR, c = lane % CR;
+            const int at = r < last ? r : last;
+            load_to_lds(kr, (u32)(at * (int)a.k_stride + 8 * (c ^ k_swizzle<D>(r))) * 2, lds_address(lds_k + b * BUF + r0 * D));
+            load_to_lds(vr, (u32)(at * (int)a.v_stride + 8 * (c ^ v_swizzle<D>(r))) * 2, lds_address(lds_v + b * BUF + r0 * D));
+        }
     };
-    auto store_k = [&](int j, const u32x4 (&w)[CH]) {
-        f16* p = lds_k + (j & 1) * KBUF + sr * K_ROW<D> + scol;
+    // In a tile that not every row sees, values that are not finite must not
+    // meet a probability of zero (their product is NaN): they are cleared,
+    // and the rows that do see their key get a NaN score.
+    auto partial = [&](int j) { return blo + j * BN + BN - 1 > row0 || blo + j * BN < blate; };
+    auto clean = [&](int j, int b) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) *reinterpret_cast<u32x4*>(p + i * ROWS * K_ROW<D>) = w[i];
-    };
-    auto store_v = [&](int j, u32x4 (&w)[CH]) {
-        // In a tile that not every row sees, values that are not finite must
-        // not meet a probability of zero (their product is NaN): they are
-        // cleared, and the rows that do see their key get a NaN score.
-        const int t0 = blo + j * BN, b = j & 1;
-        if (t0 + BN - 1 > row0 || t0 < blate) {
+        for (int i = 0; i < LOADS; ++i) {
+            const int at = i * T + tid;
+            u32x4* p = reinterpret_cast<u32x4*>(lds_v + b * BUF) + at;
+            const u32x4 v = *p;
+            bool odd = false;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                bool odd = false;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    odd = odd || (w[i][k] & 0x7C00u) == 0x7C00u || (w[i][k] & 0x7C000000u) == 0x7C000000u;
-                if (odd) {
-                    w[i] = u32x4{0, 0, 0, 0};
-                    lds_bad[b][sr + i * ROWS] = j + 1;  // of this tile: never cleared
-                    lds_any[b] = j + 1;
-                }
+            for (int k = 0; k < 4; ++k)
+                odd = odd || (v[k] & 0x7C00u) == 0x7C00u || (v[k] & 0x7C000000u) == 0x7C000000u;
+            if (odd) {
+                *p = u32x4{0, 0, 0, 0};
+                lds_bad[b][at / CR] = j + 1;  // of this tile: never cleared
+                lds_any[b] = j + 1;
             }
         }
-        f16* p = lds_v + b * VBUF + sr * V_ROW<D> + scol;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) *reinterpret_cast<u32x4*>(p + i * ROWS * V_ROW<D>) = w[i];
+        __syncthreads();
     };
 
-    // One step of 32 keys, t..t+31, in half u of the tile.
-    const f16* const k_lane = lds_k + l32 * K_ROW<D> + 8 * h;
-    const f16* const v_lane = lds_v + (4 * h + (lane >> 2 & 3)) * V_ROW<D> + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
+    // Scores of 32 keys, half u of the tile in buffer b.
+    const int k_lane = l32 * D + 8 * (h ^ k_swizzle<D>(l32));
+    const int q16 = lane & 15, v_row = 4 * h + (q16 >> 2);
+    const int v_lane = v_row * D + 8 * ((2 * (lane >> 4 & 1) + (q16 >> 1 & 1)) ^ v_swizzle<D>(v_row)) + 4 * (q16 & 1);
+    // One step of 32 keys, number u of tile j, which lies in buffer j & 1.
     auto step = [&](int j, int u) {
         const int t = blo + j * BN + 32 * u;
         if (t > whi || t + 31 < wlo) return;
         const int b = j & 1;
-        const f16* kb = k_lane + b * KBUF + 32 * u * K_ROW<D>;
+        const f16* kb = lds_k + b * BUF + 32 * u * D;
         f32x16 s = {};
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-            s = mfma32(*reinterpret_cast<const f16x8*>(kb + 16 * i), __builtin_bit_cast(f16x8, qw[i]), s);
+            s = mfma32(*reinterpret_cast<const f16x8*>(kb + (k_lane ^ (16 * i))), __builtin_bit_cast(f16x8, qw[i]), s);
         if (t + 31 > wrow0 || t < wlate) {  // not every row sees every key
             const bool bad = lds_any[b] == j + 1;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int key = t + 8 * (i / 4) + 4 * h + i % 4;
-                if (bad && lds_bad[b][32 * u + key - t] == j + 1) s[i] = __builtin_nanf("");
-                if (key > row || key < start || start < 0) s[i] = NEG_INF;
+                const int k = 8 * (i / 4) + 4 * h + i % 4;
+                if (bad && lds_bad[b][32 * u + k] == j + 1) s[i] = __builtin_nanf("");
+                if (t + k > row || t + k < start || start < 0) s[i] = NEG_INF;
             }
         }
         float top = fmaxf(s[0], s[1]);
@@ -281,68 +305,66 @@ __global__ void __launch_bounds__(64 * RW * KW, 2) attn_prompt_kernel(PromptArgs
         // 16 e + 4 h + 0..3 and + 8..11.  The transposing read takes four
         // rows of 16 values per 16 lanes, 8 bytes from each lane, and gives
         // lane i the four rows' value i.
-        const f16* vb = v_lane + b * VBUF + 32 * u * V_ROW<D>;
+        const f16* vb = lds_v + b * BUF + 32 * u * D;
         typedef __attribute__((address_space(3))) s16x4* lds_ptr;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const f16x8 pf = __builtin_bit_cast(f16x8, u32x4{w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]});
 #pragma unroll
             for (int n = 0; n < D / 32; ++n) {
-                const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vb + 16 * e * V_ROW<D> + 32 * n));
-                const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vb + (16 * e + 8) * V_ROW<D> + 32 * n));
+                const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vb + 16 * e * D + (v_lane ^ (32 * n))));
+                const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vb + (16 * e + 8) * D + (v_lane ^ (32 * n))));
                 o[n] = mfma32(__builtin_bit_cast(f16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)), pf, o[n]);
             }
         }
     };
-    // Keys and values of the next tile are on their way while this one is
-    // worked on, and go to the other buffer: one barrier per tile.
-    u32x4 kr[CH], vr[CH];
-    load_tile(kp, a.k_stride, 0, kr);
-    load_tile(vp, a.v_stride, 0, vr);
-    store_k(0, kr);
-    store_v(0, vr);
-    if (tiles > 1) load_tile(kp, a.k_stride, 1, kr);
+
+    // The next tile is on its way while this one is worked on.  Waves meet
+    // once per tile: each has waited for its own loads, so the tile is whole,
+    // and none reads the other buffer any more, so it can be filled.
+    fetch(0, 0);
     for (int j = 0; j < tiles; ++j) {
-        const bool more = j + 1 < tiles;
+        __builtin_amdgcn_s_waitcnt(WAIT_LOADS);
         __syncthreads();
-        if (more) {
-            store_k(j + 1, kr);
-            load_tile(vp, a.v_stride, j + 1, vr);
-        }
+        if (j + 1 < tiles) fetch(j + 1, (j + 1) & 1);
+        if (partial(j)) clean(j, j & 1);
+        constexpr int U = BN / 32;
 #pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-            if (KW == 1 || u == kw) step(j, u);
-            if (u == 0 && more) {
-                store_v(j + 1, vr);
-                if (j + 2 < tiles) load_tile(kp, a.k_stride, j + 2, kr);
-            }
-        }
+        for (int u = 0; u < U; ++u)
+            if (KW == 1 || u % KW == kw) step(j, u);
     }
     sum += __shfl_xor(sum, 32, 64);
-    if constexpr (KW == 2) {
-        // The second wave of each pair hands its sums over.
-        static_assert(RW * 32 * (D + 4) * 4 <= (int)sizeof lds, "room for one wave's sums of each pair");
-        float* const mine = reinterpret_cast<float*>(lds) + rw * 32 * (D + 4);
+    if constexpr (KW > 1) {
+        // The waves that share rows hand their sums to the first of them.
+        constexpr int EACH = 32 * (D + 4);  // floats: 16 D / 32 per lane, maximum and sum
+        static_assert(RW * (KW - 1) * EACH * 4 <= (int)sizeof lds, "room for their sums");
+        float* const sums = reinterpret_cast<float*>(lds) + rw * (KW - 1) * EACH + lane;
         __syncthreads();
-        if (kw == 1) {
-            mine[D * 32 + lane] = mx;
-            mine[D * 32 + 64 + lane] = sum;
+        if (kw > 0) {
+            float* const mine = sums + (kw - 1) * EACH;
+            mine[D * 32] = mx;
+            mine[D * 32 + 64] = sum;
 #pragma unroll
             for (int n = 0; n < D / 32; ++n)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) mine[(16 * n + i) * 64 + lane] = o[n][i];
+                for (int i = 0; i < 16; ++i) mine[(16 * n + i) * 64] = o[n][i];
         }
         __syncthreads();
-        if (kw == 1) return;
-        const float m1 = mine[D * 32 + lane], s1 = mine[D * 32 + 64 + lane];
-        const float m2 = fmaxf(mx, m1);
-        const float f0 = mx == NEG_INF ? 0.f : __builtin_amdgcn_exp2f((mx - m2) * sc);
-        const float f1 = m1 == NEG_INF ? 0.f : __builtin_amdgcn_exp2f((m1 - m2) * sc);
-        sum = sum * f0 + s1 * f1;
+        if (kw > 0) return;
+#pragma unroll 1
+        for (int w = 0; w < KW - 1; ++w) {
+            const float* const theirs = sums + w * EACH;
+            const float m1 = theirs[D * 32], s1 = theirs[D * 32 + 64];
+            const float m2 = fmaxf(mx, m1);
+            const float f0 = mx == NEG_INF ? 0.f : __builtin_amdgcn_exp2f((mx - m2) * sc);
+            const float f1 = m1 == NEG_INF ? 0.f : __builtin_amdgcn_exp2f((m1 - m2) * sc);
+            mx = m2;
+            sum = sum * f0 + s1 * f1;
 #pragma unroll
-        for (int n = 0; n < D / 32; ++n)
+            for (int n = 0; n < D / 32; ++n)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[n][i] = o[n][i] * f0 + mine[(16 * n + i) * 64 + lane] * f1;
+                for (int i = 0; i < 16; ++i) o[n][i] = o[n][i] * f0 + theirs[(16 * n + i) * 64] * f1;
+        }
     }
     if (start < 0) return;
     const float inv = 1.f / sum;
@@ -358,22 +380,33 @@ __global__ void __launch_bounds__(64 * RW * KW, 2) attn_prompt_kernel(PromptArgs
         }
 }
 
-template <int D, int RW, int KW>
+template <int D, int RW, int KW, int BN>
 hipError_t launch(const PromptArgs& a, hipStream_t st) {
     constexpr int BM = RW * 32;
-    const dim3 grid((unsigned)((a.tokens + BM - 1) / BM * a.q_heads));
-    attn_prompt_kernel<D, RW, KW><<<grid, 64 * RW * KW, 0, st>>>(a);
+    const dim3 grid(a.kv_heads, a.q_heads / a.kv_heads, (unsigned)((a.tokens + BM - 1) / BM));
+    attn_prompt_kernel<D, RW, KW, BN><<<grid, 64 * RW * KW, 0, st>>>(a);
     return hipGetLastError();
+}
+
+// Work-groups of 128 rows where they fill the device, else of 64 with two
+// waves for every 32 rows, which halves the longest chain of steps (2048
+// tokens, 16 heads of 128: 50 us against 54; 512 tokens, 32 heads of 64: 14.3
+// against 15.4; 4 x 4096 tokens, 16 heads of 128 the other way: 448 against
+// 328).  Tiles of 32 keys let three work-groups share a compute unit at head
+// size 128 (8192 tokens, 32 heads: 564 us against 594 with 64 keys and two);
+// at 64 four fit either way, and fewer meetings win (348 us against 350, 9
+// packed prompts of up to 700 tokens 42.8 against 45.1).
+template <int D>
+hipError_t launch_rows(const PromptArgs& a, hipStream_t st) {
+    const int64_t blocks = (a.tokens + 127) / 128 * a.q_heads;
+    if (blocks * 2 < 3 * (int64_t)a.cus && a.tokens <= 65535 * 64) return launch<D, 2, 2, 64>(a, st);
+    return launch<D, 4, 1, D == 128 ? 32 : 64>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_attn_prompt(const PromptArgs& a, hipStream_t st) {
-#ifndef PW
-#define PW 4
-#define PR 1
-#endif
-    return a.head_dim == 64 ? launch<64, PW, PR>(a, st) : launch<128, PW, PR>(a, st);
+    return a.head_dim == 64 ? launch_rows<64>(a, st) : launch_rows<128>(a, st);
 }
 
 }  // namespace qmm

@@ -304,7 +304,7 @@ qmm_status qmm_attn_prompt(const void* q, const void* k, const void* v, const in
     CHECK(std::isfinite(scale), QMM_ERR_INVALID_ARGUMENT, "scale is not finite");
     CHECK(tokens >= 0 && n_seqs >= 0 && n_seqs < 0x7ffffffe, QMM_ERR_INVALID_ARGUMENT, "tokens=%lld or n_seqs=%lld out of range",
           (long long)tokens, (long long)n_seqs);
-    CHECK(tokens <= 0x7fff0000 && (tokens + 127) / 128 * q_heads <= MAX_BLOCKS, QMM_ERR_UNSUPPORTED,
+    CHECK(tokens <= 65535 * 128 && (tokens + 127) / 128 * q_heads <= MAX_BLOCKS, QMM_ERR_UNSUPPORTED,
           "tokens=%lld with %d heads are more than one launch covers", (long long)tokens, q_heads);
     if (tokens == 0 || n_seqs == 0) return report(QMM_OK, "");
     if ((st = check_rows("q", q, q_stride, (int64_t)q_heads * head_dim, 2)) != QMM_OK) return st;
@@ -318,7 +318,7 @@ qmm_status qmm_attn_prompt(const void* q, const void* k, const void* v, const in
     int cus = 0;
     if ((st = current_cus(&cus)) != QMM_OK) return st;
     PromptArgs a{q, k, v, out, seq_offsets, tokens, n_seqs, q_stride, k_stride, v_stride, out_stride, q_heads, kv_heads,
-                 head_dim, scale};
+                 head_dim, scale, cus};
     return launched(launch_attn_prompt(a, static_cast<hipStream_t>(stream)), "qmm_attn_prompt");
 }
 

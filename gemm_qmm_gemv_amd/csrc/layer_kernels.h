@@ -78,6 +78,7 @@ struct PromptArgs {
     int64_t tokens, n_seqs, q_stride, k_stride, v_stride, out_stride;
     int q_heads, kv_heads, head_dim;
     float scale;
+    int cus;
 };
 hipError_t launch_attn_prompt(const PromptArgs& a, hipStream_t st);
 
