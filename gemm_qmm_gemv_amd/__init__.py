@@ -22,7 +22,7 @@ __all__ = [
     "qmm_gemm_f16out",
     "qmm_moe_swiglu", "qmm_gemv_residual", "qmm_moe_combine", "qmm_gemm_grouped",
     "qmm_gemm_grouped_workspace_bytes", "qmm_gemm_noalloc", "qmm_set_override", "overrides",
-    "QMM_NOALLOC_SCRATCH_BYTES",
+    "QMM_NOALLOC_SCRATCH_BYTES", "QMM_ATTN_COUNTER_BYTES",
     "KvCache", "qmm_norm_residual", "qmm_kv_append", "qmm_attn_cache", "qmm_attn_cache_workspace_bytes",
     "qmm_attn_prompt",
     "qmm_get_plan", "qmm_status_string", "qmm_last_error", "qmm_abi_version",
@@ -36,6 +36,7 @@ QMM_ERR_UNSUPPORTED = 2
 QMM_ERR_MISALIGNED = 3
 QMM_ERR_DEVICE = 4
 QMM_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # include/qmm.h
+QMM_ATTN_COUNTER_BYTES = 64 * 1024  # include/qmm.h
 
 EXPORTED_SYMBOLS = (
     "qmm_gemv", "qmm_gemm", "qmm_gemm_workspace_bytes", "qmm_moe_gemm", "qmm_unpack",

@@ -98,28 +98,39 @@ qmm_status check_rows(const char* name, const void* p, int64_t stride, int64_t w
     return QMM_OK;
 }
 
-// How qmm_attn_cache is cut.  Runs of cached rows are made short enough that
-// every compute unit gets work-groups, but no shorter than one step of every
-// wave; without a workspace for their partial sums there is one run.
-constexpr int CACHE_STEP = 128;  // cached rows that a work-group's waves take per step
+// How qmm_attn_cache is cut: as many work-groups as the device holds at once
+// share all steps evenly.  The sums of runs that
+// begin or end inside a unit need workspace; without enough of it every unit
+// gets a work-group of its own.
+constexpr int64_t COUNTERS = QMM_ATTN_COUNTER_BYTES / 4;
 
-int64_t part_bytes(int64_t units, int splits, int head_dim) { return units * splits * 16 * (head_dim + 2) * 4; }
+struct CachePlan {
+    int64_t groups;
+    bool share;
+    int row_tiles;
+    size_t bytes;  // of workspace, if shared
+};
 
-CacheAttnShape plan_attn_cache(int64_t n_seqs, int q_len, int q_heads, int kv_heads, int head_dim, int64_t max_len,
-                               int cus, size_t ws_bytes) {
-    CacheAttnShape sh;
-    sh.row_tiles = (q_len * (q_heads / kv_heads) + 15) / 16;
-    sh.units = n_seqs * kv_heads * sh.row_tiles;
-    const int64_t steps = (max_len + CACHE_STEP - 1) / CACHE_STEP;
-    int64_t splits = (4LL * cus + sh.units - 1) / sh.units;
-    if (splits > steps) splits = steps;
-    if (splits > 256) splits = 256;
-    if (splits < 1) splits = 1;
-    while (splits > 1 && part_bytes(sh.units, (int)splits, head_dim) > (int64_t)ws_bytes) --splits;
-    const int64_t per = steps == 0 ? 1 : (steps + splits - 1) / splits;
-    sh.chunk = (int)(per * CACHE_STEP);
-    sh.splits = steps == 0 ? 1 : (int)((steps + per - 1) / per);
-    return sh;
+size_t share_bytes(int64_t groups, int head_dim) {
+    return (size_t)(QMM_ATTN_COUNTER_BYTES + groups * 2 * 16 * (head_dim + 2) * 4);
+}
+
+CachePlan plan_attn_cache(const qmm_kv_cache* c, int64_t n_seqs, int q_len, int q_heads, int64_t max_len, int cus,
+                          size_t ws_bytes) {
+    CachePlan p;
+    p.row_tiles = (q_len * (q_heads / c->kv_heads) + 15) / 16;
+    const int64_t units = n_seqs * c->kv_heads * p.row_tiles;
+    const int64_t steps = units * ((max_len + CACHE_STEP - 1) / CACHE_STEP);  // at most
+    p.groups = (int64_t)cus * cache_resident(c->bits, c->head_dim);
+    if (p.groups > COUNTERS) p.groups = COUNTERS;
+    if (p.groups > steps) p.groups = steps;
+    while (p.groups > 0 && share_bytes(p.groups, c->head_dim) > ws_bytes) p.groups = p.groups * 3 / 4;
+    p.bytes = share_bytes(p.groups, c->head_dim);
+    // One run per unit: units of one step, no workspace to speak of, or more
+    // steps than 32 bits count.
+    p.share = max_len > CACHE_STEP && p.groups > units / 8 + 1 && steps < (1 << 28);
+    if (!p.share) p.groups = units;
+    return p;
 }
 
 qmm_status check_attn_cache(const qmm_kv_cache* c, bool arrays, int64_t n_seqs, int q_len, int q_heads, int64_t max_len) {
@@ -250,9 +261,8 @@ size_t qmm_attn_cache_workspace_bytes(const qmm_kv_cache* cache, int64_t n_seqs,
     int cus = 0;
     if (current_cus(&cus) != QMM_OK) cus = 256;
     (void)report(QMM_OK, "");
-    const CacheAttnShape sh = plan_attn_cache(n_seqs, q_len, q_heads, cache->kv_heads, cache->head_dim, max_kv_len, cus,
-                                              SIZE_MAX / 2);
-    return sh.splits > 1 ? (size_t)part_bytes(sh.units, sh.splits, cache->head_dim) : 0;
+    const CachePlan plan = plan_attn_cache(cache, n_seqs, q_len, q_heads, max_kv_len, cus, SIZE_MAX);
+    return plan.share ? plan.bytes : 0;
 }
 
 qmm_status qmm_attn_cache(const qmm_kv_cache* cache, const void* q, const int32_t* page_table, int64_t table_stride,
@@ -283,13 +293,18 @@ qmm_status qmm_attn_cache(const qmm_kv_cache* cache, const void* q, const int32_
     a.lens = kv_lens;
     a.table_stride = table_stride;
     a.out = out;
-    a.part = static_cast<float*>(workspace);
+    a.count = static_cast<int*>(workspace);
+    a.part = static_cast<float*>(workspace) + COUNTERS;
     a.n_seqs = n_seqs;
     a.max_len = (int)max_kv_len;
     a.q_len = q_len;
     a.q_heads = q_heads;
     a.scale = scale;
-    a.sh = plan_attn_cache(n_seqs, q_len, q_heads, cache->kv_heads, cache->head_dim, max_kv_len, cus, workspace_bytes);
+    const CachePlan plan = plan_attn_cache(cache, n_seqs, q_len, q_heads, max_kv_len, cus, workspace_bytes);
+    a.group = q_heads / cache->kv_heads;
+    a.row_tiles = plan.row_tiles;
+    a.groups = plan.groups;
+    a.share = plan.share;
     return launched(launch_attn_cache(a, static_cast<hipStream_t>(stream)), "qmm_attn_cache");
 }
 

@@ -51,23 +51,28 @@ struct AppendArgs {
 };
 hipError_t launch_append(const AppendArgs& a, hipStream_t st);
 
-// How qmm_attn_cache cuts its work: `units` (sequence, kv head, 16-row tile)
-// triples, each over `splits` runs of `chunk` cached rows.
-struct CacheAttnShape {
-    int64_t units;
-    int row_tiles, splits, chunk;
-};
+// qmm_attn_cache's work is cut into units (sequence, kv head, tile of 16 query
+// rows) and those into steps of CACHE_STEP cached rows.
+constexpr int CACHE_STEP = 128;
+// Work-groups of its kernel that one compute unit holds.
+constexpr int cache_resident(int bits, int head_dim) {
+    return head_dim == 64 ? 4 : bits == 4 ? 3 : 2;
+}
 struct CacheAttnArgs {
     CacheView c;
     const void* q;
     const int32_t *table, *lens;
     int64_t table_stride;
     void* out;
-    float* part;  // partial sums of split runs, or null
+    int* count;   // [groups] runs handed in, zero between calls
+    float* part;  // [groups][2] sums of runs, [16][head_dim + 2] each
     int64_t n_seqs;
     int max_len, q_len, q_heads;
+    int group;      // query heads per kv head
+    int row_tiles;  // units per kv head
     float scale;
-    CacheAttnShape sh;
+    int64_t groups;  // work-groups
+    bool share;      // they share all steps evenly; else one unit each
 };
 hipError_t launch_attn_cache(const CacheAttnArgs& a, hipStream_t st);
 

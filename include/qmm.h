@@ -431,11 +431,16 @@ QMM_API qmm_status qmm_kv_append(const qmm_kv_cache *cache /* host */, const voi
  *     not finite reaches the tokens that see it and no others.
  *   max_kv_len (host): at most table_stride * page_size and below 2^30.
  *   scale multiplies the scores (before the softmax).
- *   workspace: device scratch, 16-byte aligned, for partial sums; its contents
- *     are not looked at.  With less than qmm_attn_cache_workspace_bytes() long
- *     sequences are split less, with none not at all.  Calls that overlap need
- *     a workspace each.
+ *   workspace: device scratch, 16-byte aligned, for partial sums.  Its first
+ *     QMM_ATTN_COUNTER_BYTES bytes hold arrival counters: they must be zero
+ *     before its first use (allocate it zeroed once), and every call leaves
+ *     them zero again, so one workspace serves any sequence of calls on one
+ *     stream, whatever their shapes.  With less than
+ *     qmm_attn_cache_workspace_bytes() long sequences are split less, with
+ *     none not at all.  Calls that overlap need a workspace each.
  * q_len 1 to 256.                                                           */
+#define QMM_ATTN_COUNTER_BYTES (64u * 1024u)
+
 QMM_API qmm_status qmm_attn_cache(const qmm_kv_cache *cache /* host */, const void *q,
                                   const int32_t *page_table, int64_t table_stride,
                                   const int32_t *kv_lens, int64_t max_kv_len, void *out,

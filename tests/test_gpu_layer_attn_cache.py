@@ -58,15 +58,24 @@ def expect(host, table, lens, q, q_len, hq, hkv, d, bits, group, scale):
     return o, bound
 
 
+def scratch(size):
+    """A workspace: counters zero, the rest anything."""
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:qmm.QMM_ATTN_COUNTER_BYTES] = 0
+    return ws
+
+
 def run(cache, q, table, lens, max_len, q_len, hq, scale, workspace="full"):
     n = len(lens)
     out = torch.full(q.shape, float("nan"), dtype=torch.float16, device="cuda")
     need = qmm.qmm_attn_cache_workspace_bytes(cache.handle, n, q_len, hq, max_len)
     size = {"full": need, "none": 0, "half": need // 2}[workspace]
-    ws = torch.full((max(size, 16),), 0xFF, dtype=torch.uint8, device="cuda") if size else None
+    ws = scratch(size) if size else None
     qd, td, ld = dev(q), dev(table), dev(np.asarray(lens, dtype=np.int32))
     qmm.qmm_attn_cache(cache.handle, qd, td, table.shape[1], ld, max_len, out, n, q_len, hq, scale, ws, size)
     torch.cuda.synchronize()
+    if ws is not None:
+        assert not ws[:qmm.QMM_ATTN_COUNTER_BYTES].any()
     return out.cpu().numpy()
 
 
@@ -247,7 +256,7 @@ def test_same_bits_every_time_graphs_and_streams():
     for _ in range(4):
         for o in outs:
             o.zero_()
-        ws.fill_(0xFF)
+        ws[qmm.QMM_ATTN_COUNTER_BYTES:] = 0xFF
         torch.cuda.synchronize()
         for g in graphs:
             g.replay()
