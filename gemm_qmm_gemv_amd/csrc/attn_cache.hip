@@ -26,8 +26,8 @@
 // probabilities of quantized caches go in as fp16 high and low parts: the
 // matrix cores idle most of the time, and with V's rounding in the result a
 // second one of the same size would show.
+#include "layer_device.h"
 #include "layer_kernels.h"
-#include "qmm_device.h"
 
 namespace qmm {
 namespace {
@@ -47,22 +47,9 @@ __device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
 __device__ __forceinline__ f16x8 frag(u32 a, u32 b, u32 c, u32 d) {
     return __builtin_bit_cast(f16x8, u32x4{a, b, c, d});
 }
-// Max over the four lane groups that share a query row: a swap with the same
-// value in both operands leaves one half (or every other row of 16 lanes)
-// twice in each result.
-__device__ __forceinline__ float groups_max(float v) {
-    const u32 x = __builtin_bit_cast(u32, v);
-    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    const u32 a = r[0], b = r[1];
-    const u32 y = __builtin_bit_cast(u32, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
-    const auto q = __builtin_amdgcn_permlane16_swap(y, y, false, false);
-    const u32 c = q[0], d = q[1];
-    return fmaxf(__builtin_bit_cast(float, c), __builtin_bit_cast(float, d));
-}
-__device__ __forceinline__ float groups_sum(float v) {
-    v += __shfl_xor(v, 16, 64);
-    return v + __shfl_xor(v, 32, 64);
-}
+// Max / sum over the four lane groups that share a query row.
+__device__ __forceinline__ float groups_max(float v) { return over_rows(v, [](float a, float b) { return fmaxf(a, b); }); }
+__device__ __forceinline__ float groups_sum(float v) { return over_rows(v, add_f32); }
 // a / b and the rest for 0 <= a < 2^20, 0 < b < 2^20: the quotient of the
 // floats is off by less than 1/2 over b.
 __device__ __forceinline__ int small_div(int a, int b) {

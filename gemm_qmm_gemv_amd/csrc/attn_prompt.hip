@@ -24,8 +24,8 @@
 //   keys; O^T = V^T P^T takes them as its right operand as they are, with V^T
 //   read in the same order of keys.  A query row's maximum and sum need one
 //   exchange with lane l ^ 32.
+#include "layer_device.h"
 #include "layer_kernels.h"
-#include "qmm_device.h"
 
 namespace qmm {
 namespace {
@@ -89,14 +89,9 @@ __device__ __forceinline__ void sequence_starts(const int32_t* offsets, int n_se
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// Max over lanes l and l ^ 32: the swap exchanges one operand's upper lanes
-// with the other's lower ones, so with the same value in both each result
-// holds one half twice.
+// Max over lanes l and l ^ 32.
 __device__ __forceinline__ float halves_max(float v) {
-    const u32 x = __builtin_bit_cast(u32, v);
-    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    const u32 a = r[0], b = r[1];
-    return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+    return over_halves(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // 16 bytes per lane from memory to LDS without passing through registers: lane
@@ -333,7 +328,7 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
         for (int u = 0; u < U; ++u)
             if (KW == 1 || u % KW == kw) step(j, u);
     }
-    sum += __shfl_xor(sum, 32, 64);
+    sum = over_halves(sum, add_f32);
     if constexpr (KW > 1) {
         // The waves that share rows hand their sums to the first of them.
         constexpr int EACH = 32 * (D + 4);  // floats: 16 D / 32 per lane, maximum and sum
