@@ -16,19 +16,20 @@
 // product is off by up to 0.004 rad.  Sines and cosines depend on the token
 // alone, so a work-group forms them once per token in LDS and uses them for
 // all its heads.
+#include "layer_device.h"
 #include "layer_kernels.h"
-#include "qmm_device.h"
 
 namespace qmm {
 namespace {
 
 constexpr int THREADS = 256;
 
-template <int N, class F>
-__device__ __forceinline__ float butterfly(float v, F f) {
-#pragma unroll
-    for (int o = 1; o < N; o <<= 1) v = f(v, __shfl_xor(v, o, 64));
-    return v;
+// v of lane l ^ 4: row_ror:12 brings it to the lower four of eight lanes,
+// row_ror:4 to the upper four (banks 1 and 3 of a row of 16).
+__device__ __forceinline__ float lane_xor4(float v) {
+    const int x = __builtin_bit_cast(int, v);
+    const int up = __builtin_amdgcn_mov_dpp(x, 0x12C, 0xF, 0xF, true);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(up, x, 0x124, 0xF, 0xA, false));
 }
 
 // min and max that keep a NaN.
@@ -41,13 +42,56 @@ __device__ __forceinline__ void store_half8(void* p, const float (&x)[8]) {
     *static_cast<u32x4*>(p) = u32x4{pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])};
 }
 
+// The eight values of a lane as they are in memory.
+template <bool IN16>
+struct Raw8;
+template <>
+struct Raw8<true> {
+    u32x4 w;
+};
+template <>
+struct Raw8<false> {
+    f32x4 lo, hi;
+};
+
+// `tile` tokens (1 << tile_log2) and `heads_per_block` of the q, k and v heads
+// per work-group.  A row's values are asked for one round ahead: the first
+// round's while the sines and cosines are formed.
 template <int D, int BITS, bool IN16>
-__global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a, int tile, int heads_per_block) {
+__global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a, int tile_log2, int heads_per_block) {
     constexpr int L = D / 8;  // lanes per row
-    extern __shared__ float2 trig[];  // [tile][rot/2]
+    extern __shared__ __align__(16) float2 trig[];  // [tile][rot/2]
+    const int tile = 1 << tile_log2;
     const int64_t t0 = (int64_t)blockIdx.x * tile;
     const int nt = (int)(a.tokens - t0 < tile ? a.tokens - t0 : tile);
     const int half = a.rot / 2;
+    const int heads = a.q_heads + 2 * a.c.kv_heads;
+    const int h0 = blockIdx.y * heads_per_block;
+    const int nh = heads - h0 < heads_per_block ? heads - h0 : heads_per_block;
+    const int sub = threadIdx.x % L;
+    // Row r of the work-group is token r % tile of head r / tile:
+    // neighbouring rows are neighbouring tokens of one head, whose scales and
+    // mins fall into one run of memory.
+    auto fetch = [&](int r) {
+        Raw8<IN16> x = {};
+        const int tt = r & (tile - 1), head = h0 + (r >> tile_log2);
+        if (tt >= nt || r >= tile * nh) return x;
+        const int kind = head < a.q_heads ? 0 : head < a.q_heads + a.c.kv_heads ? 1 : 2;
+        const int hh = kind == 0 ? head : kind == 1 ? head - a.q_heads : head - a.q_heads - a.c.kv_heads;
+        const void* src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+        const int64_t stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
+        const int64_t off = (t0 + tt) * stride + hh * D + sub * 8;
+        if constexpr (IN16) {
+            x.w = *reinterpret_cast<const u32x4*>(static_cast<const f16*>(src) + off);
+        } else {
+            const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(src) + off);
+            x.lo = p[0];
+            x.hi = p[1];
+        }
+        return x;
+    };
+    constexpr int ROWS = THREADS / L;
+    Raw8<IN16> ahead = fetch(threadIdx.x / L);
     for (int i = threadIdx.x; i < nt * half; i += THREADS) {
         // Turns in 64 bits, the whole ones dropped there; what is left is in
         // [-1/2, 1/2] and fits fp32.
@@ -58,36 +102,27 @@ __global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a, int tile,
     }
     __syncthreads();
 
-    const int heads = a.q_heads + 2 * a.c.kv_heads;
-    const int h0 = blockIdx.y * heads_per_block;
-    const int nh = heads - h0 < heads_per_block ? heads - h0 : heads_per_block;
-    const int sub = threadIdx.x % L;
-    // Neighbouring rows of a work-group are neighbouring tokens of one head:
-    // their scales and mins then fall into one run of memory.
-    for (int r = threadIdx.x / L; r < nt * nh; r += THREADS / L) {
-        const int tt = r % nt, head = h0 + r / nt;
+    for (int r = threadIdx.x / L; r < tile * nh; r += ROWS) {
+        const Raw8<IN16> raw = ahead;
+        ahead = fetch(r + ROWS);
+        const int tt = r & (tile - 1), head = h0 + (r >> tile_log2);
+        if (tt >= nt) continue;
         const int64_t t = t0 + tt;
         const int kind = head < a.q_heads ? 0 : head < a.q_heads + a.c.kv_heads ? 1 : 2;
         const int hh = kind == 0 ? head : kind == 1 ? head - a.q_heads : head - a.q_heads - a.c.kv_heads;
-        const void* src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-        const int64_t stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
         float x[8];
-        const int64_t off = t * stride + hh * D + sub * 8;
         if constexpr (IN16) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const f16*>(src) + off);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const f16x2 p = as_h2(w[i]);
+                const f16x2 p = as_h2(raw.w[i]);
                 x[2 * i] = (float)p[0];
                 x[2 * i + 1] = (float)p[1];
             }
         } else {
-            const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(src) + off);
-            const f32x4 u = p[0], v = p[1];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[i] = u[i];
-                x[4 + i] = v[i];
+                x[i] = raw.lo[i];
+                x[4 + i] = raw.hi[i];
             }
         }
         if (kind != 2) {
@@ -96,7 +131,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a, int tile,
                 float s = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) s += x[i] * x[i];
-                s = butterfly<L>(s, [](float p, float q) { return p + q; });
+                s = over_lanes<L>(s, add_f32);
                 const float rs = 1.f / sqrtf(s / (float)D + a.eps);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = x[i] * rs * nw[sub * 8 + i];
@@ -118,15 +153,24 @@ __global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a, int tile,
                 const int lanes = half / 8;
                 const int other = sub < lanes ? sub + lanes : sub < 2 * lanes ? sub - lanes : sub;
                 float p[8];
+                if (lanes == 8) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] = __shfl(x[i], other, L);
+                    for (int i = 0; i < 8; ++i) p[i] = dpp_move<0x128>(x[i]);  // row_ror:8
+                } else if (lanes == 4) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) p[i] = lane_xor4(x[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) p[i] = __shfl(x[i], other, L);
+                }
                 if (sub < 2 * lanes) {
                     const float sign = sub < lanes ? -1.f : 1.f;
-                    const int at = (sub < lanes ? sub : sub - lanes) * 8;
+                    const f32x4* cs = reinterpret_cast<const f32x4*>(tr + (sub < lanes ? sub : sub - lanes) * 8);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 cs = tr[at + i];
-                        x[i] = x[i] * cs.x + sign * (p[i] * cs.y);
+                    for (int i = 0; i < 4; ++i) {
+                        const f32x4 t2 = cs[i];  // two cosines with their sines
+                        x[2 * i] = x[2 * i] * t2[0] + sign * (p[2 * i] * t2[1]);
+                        x[2 * i + 1] = x[2 * i + 1] * t2[2] + sign * (p[2 * i + 1] * t2[3]);
                     }
                 }
             }
@@ -155,9 +199,15 @@ __global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a, int tile,
                 hi = max_nan(hi, x[i]);
             }
             const int span = a.c.group / 8;  // lanes per group
-            for (int o = 1; o < span; o <<= 1) {
-                lo = min_nan(lo, __shfl_xor(lo, o, 64));
-                hi = max_nan(hi, __shfl_xor(hi, o, 64));
+            if (span == 4) {
+                lo = over_lanes<4>(lo, min_nan);
+                hi = over_lanes<4>(hi, max_nan);
+            } else if (span == 8) {
+                lo = over_lanes<8>(lo, min_nan);
+                hi = over_lanes<8>(hi, max_nan);
+            } else {
+                lo = over_lanes<16>(lo, min_nan);
+                hi = over_lanes<16>(hi, max_nan);
             }
             constexpr float TOP = (float)((1 << BITS) - 1);
             const f16 m16 = (f16)lo, s16 = (f16)((hi - lo) / TOP);
@@ -192,14 +242,18 @@ __global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a, int tile,
 template <int D, int BITS>
 hipError_t launch(const AppendArgs& a, hipStream_t st) {
     const int heads = a.q_heads + 2 * a.c.kv_heads;
-    // Up to 16 tokens share their sines and cosines; with few tokens one per
-    // work-group, and the heads are cut so that the device is filled.
-    const int64_t want = 2 * (int64_t)a.cus;
-    int tile = 16;
-    while (tile > 1 && (a.tokens + tile - 1) / tile < want) tile >>= 1;
-    const int64_t tiles = (a.tokens + tile - 1) / tile;
+    // Up to 16 tokens share their sines and cosines; with fewer tokens one
+    // per work-group, and the heads are cut so that the device is filled: 16
+    // work-groups for each unit.  With 2, 4, 8 and 16 of them 8192 tokens of
+    // 32 + 2 x 4 heads of 128 into an fp16 cache took 81, 57.5, 49.4 and 47.2 us,
+    // 4096 tokens of 32 + 2 x 8 heads of 64 into 4 bits 23.5, 19.2, 19.0 and 19.1.
+    const int64_t want = 16 * (int64_t)a.cus;
+    int tile_log2 = 4;
+    while (tile_log2 > 0 && (a.tokens + (1 << tile_log2) - 1) >> tile_log2 < want) --tile_log2;
+    const int tile = 1 << tile_log2;
+    const int64_t tiles = (a.tokens + tile - 1) >> tile_log2;
     const int rows_per_pass = THREADS / (D / 8);
-    int cuts = (int)((want + tiles - 1) / tiles);
+    const int cuts = (int)((want + tiles - 1) / tiles);
     int per = (heads + cuts - 1) / cuts;
     const int least = (rows_per_pass + tile - 1) / tile;  // at least one full pass of rows
     if (per < least) per = least;
@@ -207,9 +261,9 @@ hipError_t launch(const AppendArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)tiles, (unsigned)((heads + per - 1) / per));
     const size_t lds = (size_t)tile * (a.rot / 2) * sizeof(float2);
     if (a.in_fp16)
-        append_kernel<D, BITS, true><<<grid, THREADS, lds, st>>>(a, tile, per);
+        append_kernel<D, BITS, true><<<grid, THREADS, lds, st>>>(a, tile_log2, per);
     else
-        append_kernel<D, BITS, false><<<grid, THREADS, lds, st>>>(a, tile, per);
+        append_kernel<D, BITS, false><<<grid, THREADS, lds, st>>>(a, tile_log2, per);
     return hipGetLastError();
 }
 
