@@ -4,6 +4,7 @@
 // no allocation, no synchronization, no state between calls.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "layer_kernels.h"
@@ -21,14 +22,21 @@ constexpr int64_t MAX_BLOCKS = (1LL << 24) - 1;  // of 256 threads: HIP counts a
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Compute units of the current device, asked for once per device.
+std::atomic<int> g_cus[64];
+
 qmm_status current_cus(int* cus) {
     int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess ||
-        hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || *cus <= 0) {
-        (void)hipGetLastError();
-        return report(QMM_ERR_DEVICE, "no HIP device available");
+    if (hipGetDevice(&dev) == hipSuccess) {
+        std::atomic<int>* known = dev >= 0 && dev < 64 ? &g_cus[dev] : nullptr;
+        if (known && (*cus = known->load(std::memory_order_relaxed)) > 0) return QMM_OK;
+        if (hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && *cus > 0) {
+            if (known) known->store(*cus, std::memory_order_relaxed);
+            return QMM_OK;
+        }
     }
-    return QMM_OK;
+    (void)hipGetLastError();
+    return report(QMM_ERR_DEVICE, "no HIP device available");
 }
 
 qmm_status launched(hipError_t e, const char* what) {
