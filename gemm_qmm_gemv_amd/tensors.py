@@ -10,10 +10,11 @@ import functools
 import numpy as np
 import torch
 
-from . import (QMM_OK, GemvDesc, _check, _stream, load, qmm_gemm, qmm_gemm_f16out, qmm_gemm_workspace_bytes, qmm_gemv, qmm_gemv_batch_prepare,
+from . import (QMM_OK, GemvDesc, KvCache, _check, _stream, load, qmm_attn_cache, qmm_attn_cache_workspace_bytes,
+               qmm_attn_prompt, qmm_gemm, qmm_gemm_f16out, qmm_gemm_workspace_bytes, qmm_gemv, qmm_gemv_batch_prepare,
                qmm_gemv_swiglu, qmm_moe_swiglu, qmm_gemv_residual, qmm_moe_combine, qmm_gemm_grouped,
                qmm_gemm_grouped_workspace_bytes,
-               qmm_gemv_batched, qmm_moe_gemm, qmm_unpack)
+               qmm_gemv_batched, qmm_kv_append, qmm_moe_gemm, qmm_norm_residual, qmm_unpack)
 
 
 def device_tensor(a: np.ndarray, device="cuda") -> torch.Tensor:
@@ -138,6 +139,109 @@ def unpack(dq: dict, stream=None) -> torch.Tensor:
     codes = torch.empty((dq["n"], dq["k"]), dtype=torch.uint8, device=dq["w"].device)
     qmm_unpack(dq["w"], codes, dq["n"], dq["k"], dq["bits"], stream=stream)
     return codes
+
+
+def _rows(t: torch.Tensor) -> int:
+    """Elements between the token rows of t; the rest of each row is dense."""
+    dense = 1
+    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        assert size == 1 or step == dense, "rows must be dense"
+        dense *= size
+    return t.stride(0) if t.shape[0] > 1 else dense
+
+
+def norm_residual(y: torch.Tensor | None, residual: torch.Tensor | None, pre: torch.Tensor | None, eps: float = 1e-6,
+                  post: torch.Tensor | None = None, gate: torch.Tensor | None = None, scale: float = 1.0,
+                  h: torch.Tensor | None = None, x: torch.Tensor | None = None, stream=None):
+    """(h, x): h = residual + scale * gate * rmsnorm(y), x = fp16(rmsnorm(h) * pre), in one launch.
+
+    y fp32 or fp16 rows (a column range of a wider tensor will do), None: h is
+    the residual as it is; post None: y without a norm; gate [n] or [rows, n];
+    h may be the residual (updated in place)."""
+    like = residual if y is None else y
+    rows, n = like.shape
+    if y is None:
+        h = residual
+    elif h is None:
+        h = torch.empty((rows, n), dtype=torch.float32, device=y.device)
+    if x is None:
+        x = torch.empty((rows, n), dtype=torch.float16, device=like.device)
+    qmm_norm_residual(y, y is not None and y.dtype == torch.float16, 0 if y is None else _rows(y), post, gate,
+                      _rows(gate) if gate is not None and gate.dim() == 2 else 0, scale, residual,
+                      None if y is None else h, pre, x, rows, n, eps, stream=stream)
+    return h, x
+
+
+def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, bits: int = 4, group: int = 64,
+             device="cuda") -> KvCache:
+    """A paged key/value cache of zeros (the handle keeps its tensors)."""
+    def rows():
+        return torch.zeros((pages, kv_heads, page_size, head_dim * bits // 32), dtype=torch.int32, device=device)
+
+    def meta():
+        if bits == 16:
+            return None
+        return torch.zeros((pages, kv_heads, head_dim // group, page_size), dtype=torch.float16, device=device)
+
+    return KvCache(rows(), meta(), meta(), rows(), meta(), meta(), pages, kv_heads, head_dim, page_size, bits, group)
+
+
+def kv_append(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
+              slots: torch.Tensor | None, inv_freq: torch.Tensor | None = None, interleaved: bool = False,
+              q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None, eps: float = 1e-6,
+              out: torch.Tensor | None = None, prompt_rows: bool = False, cached_values: bool = False, stream=None):
+    """New tokens' rows q, k and v [tokens, heads * head_dim] (column ranges of one fused product will do): returns the
+    normed and rotated queries [tokens, q_heads, head_dim] and stores keys and values in `slots`.  With prompt_rows it
+    returns (q, k, v) for attn_prompt, k and v as the cache stands for them if cached_values."""
+    tokens, d = q.shape[0], cache.head_dim
+    q_heads = q[0].numel() // d if tokens else q.shape[-1] // d
+    assert q.dtype == k.dtype == v.dtype
+    if out is None:
+        out = torch.empty((tokens, q_heads, d), dtype=torch.float16, device=q.device)
+    k_out = v_out = None
+    if prompt_rows:
+        k_out = torch.empty((tokens, cache.kv_heads, d), dtype=torch.float16, device=q.device)
+        v_out = torch.empty_like(k_out)
+    qmm_kv_append(cache, q, k, v, q.dtype == torch.float16, _rows(q), _rows(k), _rows(v), q_norm, k_norm, eps,
+                  inv_freq, 0 if inv_freq is None else 2 * inv_freq.numel(), interleaved, positions, slots, out,
+                  k_out, v_out, cached_values, tokens, q_heads, stream=stream)
+    return (out, k_out, v_out) if prompt_rows else out
+
+
+def attn_workspace(cache: KvCache, n_seqs: int, q_len: int, q_heads: int, max_kv_len: int,
+                   device="cuda") -> torch.Tensor:
+    """Scratch for attn_cache calls up to this size, one after another on one stream."""
+    need = qmm_attn_cache_workspace_bytes(cache, n_seqs, q_len, q_heads, max_kv_len)
+    # Zeroed: the arrival counters at its start must read zero before the
+    # first call (every call leaves them zero).
+    return torch.zeros(max(need, 16), dtype=torch.uint8, device=device)
+
+
+def attn_cache(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, max_kv_len: int,
+               scale: float | None = None, q_len: int = 1, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of q [n_seqs * q_len, q_heads, head_dim], each sequence's newest q_len tokens, over the cache."""
+    n_seqs, q_heads = kv_lens.shape[0], q.shape[-2]
+    assert q.is_contiguous() and q.numel() == n_seqs * q_len * q_heads * cache.head_dim
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        workspace = attn_workspace(cache, n_seqs, q_len, q_heads, max_kv_len, q.device)
+    qmm_attn_cache(cache, q, page_table, page_table.stride(0) if n_seqs > 1 else page_table.shape[1], kv_lens,
+                   max_kv_len, out, n_seqs, q_len, q_heads, cache.head_dim ** -0.5 if scale is None else scale,
+                   workspace, workspace.numel() * workspace.element_size(), stream=stream)
+    return out
+
+
+def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_offsets: torch.Tensor,
+                scale: float | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention in each of the sequences packed in q [tokens, q_heads, d], k and v [tokens, kv_heads, d]."""
+    tokens, q_heads, d = q.shape
+    if out is None:
+        out = torch.empty((tokens, q_heads, d), dtype=torch.float16, device=q.device)
+    qmm_attn_prompt(q, k, v, seq_offsets, out, tokens, seq_offsets.numel() - 1, q_heads, k.shape[1], d, _rows(q),
+                    _rows(k), _rows(v), _rows(out), d ** -0.5 if scale is None else scale, stream=stream)
+    return out
 
 
 class GemvBatch:
