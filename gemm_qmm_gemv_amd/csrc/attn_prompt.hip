@@ -8,7 +8,7 @@
 // have about the same load.  Short steps on many waves keep all three busy
 // best: a wave holds 32 query rows of one head and takes 32 keys a step, and
 // three (head size 128) or four waves on each SIMD are at different places of
-// it.  8192 tokens, 32 query and 4 key heads of 128: 564 us, 975 TFLOP/s, 83 %
+// it.  8192 tokens, 32 query and 4 key heads of 128: 558 us, 985 TFLOP/s, 84 %
 // of what a large fp16 matrix product of the library reaches on the card (1178;
 // the clock drops to 1.9 GHz under either).  Tried and slower there: two waves
 // per SIMD with the next step's scores formed early (593 us), the same with
@@ -31,9 +31,6 @@ namespace qmm {
 namespace {
 
 constexpr float NEG_INF = -__builtin_huge_valf();
-// s_waitcnt: all vector memory done (expcnt and lgkmcnt not waited on).
-constexpr int WAIT_LOADS = 0x0F70;
-
 typedef f16 f16x4v __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
@@ -225,7 +222,8 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
     };
     // In a tile that not every row sees, values that are not finite must not
     // meet a probability of zero (their product is NaN): they are cleared,
-    // and the rows that do see their key get a NaN score.
+    // and the rows that do see their key get a NaN score.  A thread looks at
+    // the chunks that it loaded itself, before the waves meet.
     auto partial = [&](int j) { return blo + j * BN + BN - 1 > row0 || blo + j * BN < blate; };
     auto clean = [&](int j, int b) {
 #pragma unroll
@@ -233,17 +231,15 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
             const int at = i * T + tid;
             u32x4* p = reinterpret_cast<u32x4*>(lds_v + b * BUF) + at;
             const u32x4 v = *p;
-            bool odd = false;
+            u32 odd = 0;  // an exponent of ones carries into the sign's place
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                odd = odd || (v[k] & 0x7C00u) == 0x7C00u || (v[k] & 0x7C000000u) == 0x7C000000u;
-            if (odd) {
+            for (int k = 0; k < 4; ++k) odd |= (v[k] & 0x7C007C00u) + 0x04000400u;
+            if (odd & 0x80008000u) {
                 *p = u32x4{0, 0, 0, 0};
                 lds_bad[b][at / CR] = j + 1;  // of this tile: never cleared
                 lds_any[b] = j + 1;
             }
         }
-        __syncthreads();
     };
 
     // Scores of 32 keys, half u of the tile in buffer b.
@@ -261,13 +257,17 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
         for (int i = 0; i < D / 16; ++i)
             s = mfma32(*reinterpret_cast<const f16x8*>(kb + (k_lane ^ (16 * i))), __builtin_bit_cast(f16x8, qw[i]), s);
         if (t + 31 > wrow0 || t < wlate) {  // not every row sees every key
-            const bool bad = lds_any[b] == j + 1;
+            if (__builtin_expect(uniform(lds_any[b]) == j + 1, 0)) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int k = 8 * (i / 4) + 4 * h + i % 4;
-                if (bad && lds_bad[b][32 * u + k] == j + 1) s[i] = __builtin_nanf("");
-                if (t + k > row || t + k < start || start < 0) s[i] = NEG_INF;
+                for (int i = 0; i < 16; ++i)
+                    if (lds_bad[b][32 * u + 8 * (i / 4) + 4 * h + i % 4] == j + 1) s[i] = __builtin_nanf("");
             }
+            // This row sees key t + k if start <= t + k <= row: one unsigned
+            // comparison of its distance from the start.
+            const u32 seen = start < 0 ? 0 : (u32)(row - start + 1), from_start = (u32)(t + 4 * h - start);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (from_start + (u32)(8 * (i / 4) + i % 4) >= seen) s[i] = NEG_INF;
         }
         float top = fmaxf(s[0], s[1]);
 #pragma unroll
@@ -319,10 +319,10 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
     // and none reads the other buffer any more, so it can be filled.
     fetch(0, 0);
     for (int j = 0; j < tiles; ++j) {
-        __builtin_amdgcn_s_waitcnt(WAIT_LOADS);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (partial(j)) clean(j, j & 1);
         __syncthreads();
         if (j + 1 < tiles) fetch(j + 1, (j + 1) & 1);
-        if (partial(j)) clean(j, j & 1);
         constexpr int U = BN / 32;
 #pragma unroll 1
         for (int u = 0; u < U; ++u)
@@ -385,12 +385,12 @@ hipError_t launch(const PromptArgs& a, hipStream_t st) {
 
 // Work-groups of 128 rows where they fill the device, else of 64 with two
 // waves for every 32 rows, which halves the longest chain of steps (2048
-// tokens, 16 heads of 128: 50 us against 54; 512 tokens, 32 heads of 64: 14.3
-// against 15.4; 4 x 4096 tokens, 16 heads of 128 the other way: 448 against
-// 328).  Tiles of 32 keys let three work-groups share a compute unit at head
-// size 128 (8192 tokens, 32 heads: 564 us against 594 with 64 keys and two);
-// at 64 four fit either way, and fewer meetings win (348 us against 350, 9
-// packed prompts of up to 700 tokens 42.8 against 45.1).
+// tokens, 16 heads of 128: 44 us against 57; 512 tokens, 32 heads of 64: 12.2
+// against 15.0; 4 x 4096 tokens, 16 heads of 128 the other way: 418 against
+// 330).  Tiles of 32 keys let three work-groups share a compute unit at head
+// size 128 (8192 tokens, 32 heads: 558 us against 594 with 64 keys and two);
+// at 64 four fit either way, and fewer meetings win (343 us against 350, 9
+// packed prompts of up to 700 tokens 33.2 against 34.6).
 template <int D>
 hipError_t launch_rows(const PromptArgs& a, hipStream_t st) {
     const int64_t blocks = (a.tokens + 127) / 128 * a.q_heads;
