@@ -9,8 +9,18 @@
 // and the new tokens of a sequence are the rows of one 16-row matrix tile, so
 // a cached row is read and unpacked once for all of them.  A wave owns tiles
 // of 32 cached rows and keeps its own running maximum and sum, so waves meet
-// only at the end; runs of `chunk` cached rows go to different work-groups
-// and a second kernel joins their sums.
+// only at the end.  All cached rows are cut into equal shares, one per
+// resident work-group, and whoever hands in the last part of a sequence joins
+// them, in the same launch.
+//
+// 64 histories of 4000 to 16384 rows, 4 key heads of 128, 4 bits (348 MB) take 87
+// us among other calls, 4.0 TB/s; inside the loop 5.3, the rate of a copy.  The
+// rest is 6 us before the first rows arrive and the ends: of three work-groups
+// on a compute unit the first launched is done after 77 us, the last after 98 of
+// a call alone.  Tried for it and not better: priorities by what is left,
+// shares of 9, 8 and 7 eighths, a third step in flight, unpacking with fewer
+// instructions (the vector units alone would need 67 us).  Short calls are a chain
+// of waits: lengths, page table, rows, the acknowledgement of partial sums, the join.
 //
 // Matrix products (v_mfma 16x16x32 fp16, fp32 sums), transposed so that no
 // value changes lanes between the two:
@@ -668,7 +678,10 @@ __global__ void __launch_bounds__(64 * WAVES, cache_resident(BITS, D)) attn_cach
     };
     auto steps_of = [&](int len) { return (uint32_t)(len + STEP - 1) / STEP; };
     // A unit is counted as START steps more than it has: what beginning and
-    // joining a run costs.
+    // joining a run costs.  With 0, 1, 2 and 4 of them drafts over 8 bits
+    // (5 steps a share) took 28.7, 27.3, 26.3 and 26.4 us, 17 ragged sequences (2
+    // steps) 22.0, 20.0, 20.3 and 20.3, 64 long histories (25 steps) 96 to 103
+    // with any of them.
     auto size_of = [&](int len) { return len == 0 ? 0u : steps_of(len) + START; };
 
     Segment sg;
@@ -718,7 +731,8 @@ __global__ void __launch_bounds__(64 * WAVES, cache_resident(BITS, D)) attn_cach
         }
         before -= own;
         total = uniform((int)(total * per_seq));
-        // No more shares than make LEAST steps each.  Neighbouring shares go
+        // No more shares than make LEAST steps each (one sequence of 1500 rows
+        // with 1, 2 and 4: 11.4, 10.8 and 13.9 us).  Neighbouring shares go
         // to one die (work-groups go round the eight), so row tiles that read
         // the same cached rows share its L2.
         uint32_t shares = total / LEAST;
