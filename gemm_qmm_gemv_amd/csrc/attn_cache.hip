@@ -13,14 +13,12 @@
 // resident work-group, and whoever hands in the last part of a sequence joins
 // them, in the same launch.
 //
-// 64 histories of 4000 to 16384 rows, 4 key heads of 128, 4 bits (348 MB) take 87
-// us among other calls, 4.0 TB/s; inside the loop 5.3, the rate of a copy.  The
-// rest is 6 us before the first rows arrive and the ends: of three work-groups
-// on a compute unit the first launched is done after 77 us, the last after 98 of
-// a call alone.  Tried for it and not better: priorities by what is left,
-// shares of 9, 8 and 7 eighths, a third step in flight, unpacking with fewer
-// instructions (the vector units alone would need 67 us).  Short calls are a chain
-// of waits: lengths, page table, rows, the acknowledgement of partial sums, the join.
+// 64 histories of 4000 to 16384 rows, 4 key heads of 128, 4 bits (348 MB) take
+// 78 us, 4.5 TB/s.  What is left above the rate of a copy (5.3) is 6 us before the
+// first rows arrive and the ends: of the work-groups on a compute unit the one
+// that was launched first is served first and done first.  The vector units
+// alone would need 64 us.  Short calls are a chain of waits: lengths, page
+// table, rows, the acknowledgement of partial sums, the join.
 //
 // Matrix products (v_mfma 16x16x32 fp16, fp32 sums), transposed so that no
 // value changes lanes between the two:
@@ -176,13 +174,13 @@ __device__ __forceinline__ void ask(const CacheView& cv, const Place& at, const 
             rows_to_lds(k + at.rows[b], k_off, to + n * 1024);
             rows_to_lds(v + at.rows[b], v_off, to + 32 * C::ROW + n * 1024);
         } else {  // one load covers both halves
-            const int64_t half = lane < 32 ? at.rows[0] : at.rows[1];
+            const int64_t r0 = at.rows[0], r1 = at.rows[1], half = lane < 32 ? r0 : r1;
             rows_to_lds(k + half + k_off, to + n * 1024);
             rows_to_lds(v + half + v_off, to + 32 * C::ROW + n * 1024);
         }
     }
     // Per group 64 words: [K, V][8 quads of rows][scales, mins][2 pairs].
-    const int64_t half = (lane >> 4 & 1) ? at.scales[1] : at.scales[0];
+    const int64_t s0 = at.scales[0], s1 = at.scales[1], half = (lane >> 4 & 1) ? s1 : s0;
 #pragma unroll
     for (int h = 0; h < C::NG; ++h)
         words_to_lds(scales + half + ((int64_t)h << (cv.page_shift + 1)), to + 64 * C::ROW + h * 256);
@@ -299,6 +297,14 @@ __device__ constexpr int q_order(int i) {
     return i;
 }
 
+// (v & mask) | magic in one instruction (an instruction holds one constant, so
+// the compiler, which has two, makes it two).
+__device__ __forceinline__ u32 and_or(u32 v, u32 mask, u32 magic) {
+    u32 r;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(v), "s"(mask), "v"(magic));
+    return r;
+}
+
 // V^T operand of value i (of the lane's VC) at the eight cached rows.
 template <int BITS, int VW>
 __device__ __forceinline__ f16x8 v_frag(const u32 (&w)[8][VW], int i, const u32x2 (&s)[2], const u32x2 (&m)[2]) {
@@ -312,8 +318,13 @@ __device__ __forceinline__ f16x8 v_frag(const u32 (&w)[8][VW], int i, const u32x
         if constexpr (BITS == 16) {
             out[p] = x;
         } else {
-            const u32 mask = BITS == 4 ? 0x000F000Fu : 0x00FF00FFu;
-            const f16x2 code = as_h2(mask_or_magic(x >> (bit % 16), mask)) - as_h2(MAGIC2);
+            // 0x6400 + code is 1024 + code.  A nibble left at bits 4..7 under
+            // 0x5400, whose last bit stands for 1/16, is 64 + code: one
+            // shift serves two nibbles (17 ragged sequences 17.5 -> 17.3 us).
+            const bool upper = BITS == 4 && bit % 8 == 4;
+            const u32 mask = BITS == 8 ? 0x00FF00FFu : upper ? 0x00F000F0u : 0x000F000Fu;
+            const u32 magic = upper ? 0x54005400u : MAGIC2;
+            const f16x2 code = as_h2(and_or(x >> (bit % 16 & 8), mask, magic)) - as_h2(magic);
             const f16x2 sc = as_h2(s[p / 2][p % 2]), mn = as_h2(m[p / 2][p % 2]);
             out[p] = as_u32(__builtin_elementwise_fma(code, sc, mn));
         }
@@ -381,22 +392,31 @@ __device__ __forceinline__ void attend(const CacheAttnArgs& a, const Segment& sg
     const int32_t* table = a.table + seq * a.table_stride;
     const int in_page = (1 << a.c.page_shift) - 1;
     bool bad = false;
-    // Page of the 16 rows from t on.  Past the last row there is no entry to
-    // read: row t0 stands in, and what comes of it is masked.
-    auto entry = [&](int t) { return uniform(table[(t < len ? t : t0) >> a.c.page_shift]); };
-    int ahead[2];  // entries of the step that is asked for next
+    // Table entries of the wave's next 32 steps, two to a step, one per lane.
+    // (An entry asked for step by step would be waited for with everything
+    // asked for after it: the rows of the next step would never be under way
+    // while this one's are worked on.)  Past the last row there is no
+    // entry to read: that of row t0 stands in, and what comes of it is masked.
+    int entries = 0, used = 32;
     auto place = [&](int first) {
+        if (used == 32) {
+            const int t = first + (lane >> 1) * STRIDE + (lane & 1) * 16;
+            entries = table[(t < len ? t : t0) >> a.c.page_shift];
+            asm volatile("" : "+v"(entries));  // waited for here and nowhere else
+            used = 0;
+        }
         Place at;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const bool in = ahead[b] >= 0 && ahead[b] < a.c.pages;
+            const int entry = __builtin_amdgcn_readlane(entries, 2 * used + b);
+            const bool in = entry >= 0 && entry < a.c.pages;
             bad = bad || !in;
-            const int64_t unit = (int64_t)(in ? ahead[b] : 0) * a.c.kv_heads + kvh;
+            const int64_t unit = (int64_t)(in ? entry : 0) * a.c.kv_heads + kvh;
             const int row0 = (first + 16 * b) & in_page;
             at.rows[b] = ((unit << a.c.page_shift) + row0) * C::ROW;
             at.scales[b] = ((unit * C::NG << a.c.page_shift) + row0) * 2;
-            ahead[b] = entry(first + 16 * b + STRIDE);
         }
+        ++used;
         return at;
     };
 
@@ -408,8 +428,6 @@ __device__ __forceinline__ void attend(const CacheAttnArgs& a, const Segment& sg
     char* const ring = sh.ring + (C::Q ? wave * C::STAGES * C::STAGE : 0);
     int stage = 0;
     if (first < t1) {
-        ahead[0] = entry(first);
-        ahead[1] = entry(first + 16);
         if constexpr (C::Q) {
             ask<C>(a.c, place(first), scales, lds_address(ring));
         } else {
