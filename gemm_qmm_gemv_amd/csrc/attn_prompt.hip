@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
     const int q16 = lane & 15, v_row = 4 * h + (q16 >> 2);
     const int v_lane = v_row * D + 8 * ((2 * (lane >> 4 & 1) + (q16 >> 1 & 1)) ^ v_swizzle<D>(v_row)) + 4 * (q16 & 1);
     // One step of 32 keys, number u of tile j, which lies in buffer j & 1.
-    auto step = [&](int j, int u) {
+    auto step = [&](int j, int u, bool cleaned) {
         const int t = blo + j * BN + 32 * u;
         if (t > whi || t + 31 < wlo) return;
         const int b = j & 1;
@@ -256,12 +256,13 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
             s = mfma32(*reinterpret_cast<const f16x8*>(kb + (k_lane ^ (16 * i))), __builtin_bit_cast(f16x8, qw[i]), s);
-        if (t + 31 > wrow0 || t < wlate) {  // not every row sees every key
-            if (__builtin_expect(uniform(lds_any[b]) == j + 1, 0)) {
+        // (Cleared for the work-group, so marked by waves that see every key too.)
+        if (cleaned && __builtin_expect(uniform(lds_any[b]) == j + 1, 0)) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (lds_bad[b][32 * u + 8 * (i / 4) + 4 * h + i % 4] == j + 1) s[i] = __builtin_nanf("");
-            }
+            for (int i = 0; i < 16; ++i)
+                if (lds_bad[b][32 * u + 8 * (i / 4) + 4 * h + i % 4] == j + 1) s[i] = __builtin_nanf("");
+        }
+        if (t + 31 > wrow0 || t < wlate) {  // not every row sees every key
             // This row sees key t + k if start <= t + k <= row: one unsigned
             // comparison of its distance from the start.
             const u32 seen = start < 0 ? 0 : (u32)(row - start + 1), from_start = (u32)(t + 4 * h - start);
@@ -320,13 +321,14 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
     fetch(0, 0);
     for (int j = 0; j < tiles; ++j) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        if (partial(j)) clean(j, j & 1);
+        const bool cleaned = partial(j);
+        if (cleaned) clean(j, j & 1);
         __syncthreads();
         if (j + 1 < tiles) fetch(j + 1, (j + 1) & 1);
         constexpr int U = BN / 32;
 #pragma unroll 1
         for (int u = 0; u < U; ++u)
-            if (KW == 1 || u % KW == kw) step(j, u);
+            if (KW == 1 || u % KW == kw) step(j, u, cleaned);
     }
     sum = over_halves(sum, add_f32);
     if constexpr (KW > 1) {
