@@ -226,6 +226,8 @@ def attn_cache(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_len
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
+        # Made and given back on the current stream.
+        assert stream is None, "a call on another stream needs a workspace of its own"
         workspace = attn_workspace(cache, n_seqs, q_len, q_heads, max_kv_len, q.device)
     qmm_attn_cache(cache, q, page_table, page_table.stride(0) if n_seqs > 1 else page_table.shape[1], kv_lens,
                    max_kv_len, out, n_seqs, q_len, q_heads, cache.head_dim ** -0.5 if scale is None else scale,
