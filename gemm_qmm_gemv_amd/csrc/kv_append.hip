@@ -33,6 +33,35 @@ __device__ __forceinline__ float lane_xor4(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(up, x, 0x124, 0xF, 0xA, false));
 }
 
+// Sine and cosine of an angle, both rounded once: whole quarter turns are dropped
+// in 64 bits, and within an eighth of a turn the Taylor series to x^11 and
+// x^12 are off by less than 10^-11.  (As fp32 functions of an angle rounded to
+// fp32 they were off by up to two steps, which showed as minima of groups
+// that fell on the other side of a border of fp16.)
+__device__ __forceinline__ void sin_cos(double angle, float& s, float& c) {
+    const double quarters = rint(angle * 0.63661977236758134308);
+    const double x = __builtin_fma(quarters, -1.57079632679489661923, angle) - quarters * 6.123233995736766e-17;
+    const double y = x * x;
+    double p = -1.0 / 39916800, q = 1.0 / 479001600;
+    p = __builtin_fma(p, y, 1.0 / 362880);
+    p = __builtin_fma(p, y, -1.0 / 5040);
+    p = __builtin_fma(p, y, 1.0 / 120);
+    p = __builtin_fma(p, y, -1.0 / 6);
+    p = __builtin_fma(p * y, x, x);
+    q = __builtin_fma(q, y, -1.0 / 3628800);
+    q = __builtin_fma(q, y, 1.0 / 40320);
+    q = __builtin_fma(q, y, -1.0 / 720);
+    q = __builtin_fma(q, y, 1.0 / 24);
+    q = __builtin_fma(q, y, -0.5);
+    q = __builtin_fma(q, y, 1.0);
+    const int turn = (int)(quarters - 4 * floor(quarters * 0.25));  // 0 to 3
+    const float sine = (float)p, cosine = (float)q;
+    s = turn & 1 ? cosine : sine;
+    c = turn & 1 ? sine : cosine;
+    if (turn & 2) s = -s;
+    if (turn == 1 || turn == 2) c = -c;
+}
+
 // min and max that keep a NaN.
 __device__ __forceinline__ float min_nan(float a, float b) { return __builtin_elementwise_minimum(a, b); }
 __device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
@@ -94,11 +123,8 @@ __global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a, int tile_
     constexpr int ROWS = THREADS / L;
     Raw8<IN16> ahead = fetch(threadIdx.x / L);
     for (int i = threadIdx.x; i < nt * half; i += THREADS) {
-        // Turns in 64 bits, the whole ones dropped there; what is left is in
-        // [-1/2, 1/2] and fits fp32.
-        const double turns = (double)a.positions[t0 + i / half] * (double)a.inv_freq[i % half] * 0.15915494309189533577;
         float s, c;
-        sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+        sin_cos((double)a.positions[t0 + i / half] * (double)a.inv_freq[i % half], s, c);
         trig[i] = float2{c, s};
     }
     __syncthreads();

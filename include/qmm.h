@@ -391,8 +391,8 @@ typedef struct qmm_kv_cache {
  *     k_norm fp32 [head_dim] or NULL), then the rotation of the first rot_dim
  *     elements by position: with t = positions[token] * inv_freq[i], elements
  *     (a, b) = (x[i], x[i + rot_dim / 2]), or (x[2i], x[2i + 1]) if
- *     interleaved, become (a cos t - b sin t, b cos t + a sin t).  The angle is
- *     formed in 64 bits.
+ *     interleaved, become (a cos t - b sin t, b cos t + a sin t).  The angle
+ *     (below 2^50) is formed and reduced in 64 bits.
  *   q_out fp16 [tokens][q_heads][head_dim]
  *   k, v: into slot slots[token] of the cache.  Per group: min fp16(lowest),
  *     scale fp16((highest - lowest) / (2^bits - 1)), code
