@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "QmmError", "library_path", "load",
@@ -44,7 +45,7 @@ EXPORTED_SYMBOLS = (
     "qmm_moe_swiglu", "qmm_gemv_residual", "qmm_moe_combine", "qmm_gemm_grouped",
     "qmm_gemm_grouped_workspace_bytes", "qmm_gemm_noalloc", "qmm_set_override",
     "qmm_norm_residual", "qmm_kv_append", "qmm_attn_cache", "qmm_attn_cache_workspace_bytes", "qmm_attn_prompt",
-    "qmm_get_plan", "qmm_status_string", "qmm_last_error", "qmm_abi_version",
+    "qmm_call_words", "qmm_get_plan", "qmm_status_string", "qmm_last_error", "qmm_abi_version",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -180,11 +181,13 @@ def load():
     lib.qmm_attn_cache_workspace_bytes.argtypes = [pc, i64, ci, ci, i64]
     lib.qmm_attn_cache_workspace_bytes.restype = sz
     lib.qmm_attn_prompt.argtypes = [p, p, p, p, p, i64, i64, ci, ci, ci, i64, i64, i64, i64, cf, p]
+    lib.qmm_call_words.argtypes = [ci, ctypes.c_char_p]
     lib.qmm_get_plan.argtypes = [ci, i64, i64, i64, ci, ci, ci, sz, ctypes.POINTER(_Plan)]
     for f in ("qmm_gemv", "qmm_gemm", "qmm_moe_gemm", "qmm_unpack", "qmm_get_plan",
               "qmm_gemv_batch_prepare", "qmm_gemv_batched", "qmm_gemv_swiglu", "qmm_gemm_f16out", "qmm_moe_swiglu",
               "qmm_gemv_residual", "qmm_moe_combine", "qmm_gemm_grouped", "qmm_gemm_noalloc",
-              "qmm_set_override", "qmm_norm_residual", "qmm_kv_append", "qmm_attn_cache", "qmm_attn_prompt"):
+              "qmm_set_override", "qmm_norm_residual", "qmm_kv_append", "qmm_attn_cache", "qmm_attn_prompt",
+              "qmm_call_words"):
         getattr(lib, f).restype = ci
     lib.qmm_status_string.argtypes = [ci]
     lib.qmm_status_string.restype = ctypes.c_char_p
@@ -369,33 +372,56 @@ def qmm_moe_swiglu(gate_w, gate_scales, gate_mins, up_w, up_scales, up_mins, x, 
            "qmm_moe_swiglu")
 
 
+# The layer's operators go through qmm_call_words: ctypes converts every
+# argument by a call of its own, which took 4.3 us for the append's 23 (packed:
+# 2.1) where the kernel of a decode step takes 4.5.
+_NORM_WORDS = struct.Struct("=6qd6qdq").pack
+_APPEND_WORDS = struct.Struct("=10qd12q").pack
+_CACHE_WORDS = struct.Struct("=10qd3q").pack
+_PROMPT_WORDS = struct.Struct("=14qdq").pack
+
+
+def _word(v):
+    if v is None:
+        return 0
+    try:
+        return v.data_ptr()
+    except AttributeError:
+        return v  # an address
+
+
 def qmm_norm_residual(y, y_fp16, y_stride, post_weight, gate, gate_stride, scale, residual, h, pre_weight, x, rows, n,
                       eps, stream=None) -> None:
     """h = residual + scale * gate * rmsnorm(y); x = fp16(rmsnorm(h)); asynchronous."""
-    _check(load().qmm_norm_residual(_addr(y), bool(y_fp16), int(y_stride), _addr(post_weight), _addr(gate),
-                                    int(gate_stride), float(scale), _addr(residual), _addr(h), _addr(pre_weight),
-                                    _addr(x), int(rows), int(n), float(eps), _stream(stream)),
-           "qmm_norm_residual")
+    status = load().qmm_call_words(0, _NORM_WORDS(_word(y), y_fp16, y_stride, _word(post_weight), _word(gate),
+                                                  gate_stride, scale, _word(residual), _word(h), _word(pre_weight),
+                                                  _word(x), rows, n, eps, _stream(stream)))
+    if status != QMM_OK:
+        _check(status, "qmm_norm_residual")
 
 
 def qmm_kv_append(cache, q, k, v, in_fp16, q_stride, k_stride, v_stride, q_norm, k_norm, eps, inv_freq, rot_dim,
                   interleaved, positions, slots, q_out, k_out, v_out, out_cached, tokens, q_heads, stream=None) -> None:
     """Rotated queries, and keys and values into the cache's slots (``cache``: a ``KvCache``); asynchronous."""
-    _check(load().qmm_kv_append(cache, _addr(q), _addr(k), _addr(v), bool(in_fp16), int(q_stride), int(k_stride),
-                                int(v_stride), _addr(q_norm), _addr(k_norm), float(eps), _addr(inv_freq),
-                                int(rot_dim), bool(interleaved), _addr(positions), _addr(slots), _addr(q_out),
-                                _addr(k_out), _addr(v_out), bool(out_cached), int(tokens), int(q_heads),
-                                _stream(stream)),
-           "qmm_kv_append")
+    status = load().qmm_call_words(1, _APPEND_WORDS(ctypes.addressof(cache) if cache is not None else 0, _word(q),
+                                                    _word(k), _word(v), in_fp16, q_stride, k_stride, v_stride,
+                                                    _word(q_norm), _word(k_norm), eps, _word(inv_freq), rot_dim,
+                                                    interleaved, _word(positions), _word(slots), _word(q_out),
+                                                    _word(k_out), _word(v_out), out_cached, tokens, q_heads,
+                                                    _stream(stream)))
+    if status != QMM_OK:
+        _check(status, "qmm_kv_append")
 
 
 def qmm_attn_cache(cache, q, page_table, table_stride, kv_lens, max_kv_len, out, n_seqs, q_len, q_heads, scale,
                    workspace=None, workspace_bytes=0, stream=None) -> None:
     """Attention of each sequence's newest ``q_len`` tokens over its cached rows; asynchronous."""
-    _check(load().qmm_attn_cache(cache, _addr(q), _addr(page_table), int(table_stride), _addr(kv_lens),
-                                 int(max_kv_len), _addr(out), int(n_seqs), int(q_len), int(q_heads), float(scale),
-                                 _addr(workspace), int(workspace_bytes), _stream(stream)),
-           "qmm_attn_cache")
+    status = load().qmm_call_words(2, _CACHE_WORDS(ctypes.addressof(cache) if cache is not None else 0, _word(q),
+                                                   _word(page_table), table_stride, _word(kv_lens), max_kv_len,
+                                                   _word(out), n_seqs, q_len, q_heads, scale, _word(workspace),
+                                                   workspace_bytes, _stream(stream)))
+    if status != QMM_OK:
+        _check(status, "qmm_attn_cache")
 
 
 def qmm_attn_cache_workspace_bytes(cache, n_seqs, q_len, q_heads, max_kv_len) -> int:
@@ -405,10 +431,11 @@ def qmm_attn_cache_workspace_bytes(cache, n_seqs, q_len, q_heads, max_kv_len) ->
 def qmm_attn_prompt(q, k, v, seq_offsets, out, tokens, n_seqs, q_heads, kv_heads, head_dim, q_stride, k_stride,
                     v_stride, out_stride, scale, stream=None) -> None:
     """Causal attention in each of the packed sequences; asynchronous."""
-    _check(load().qmm_attn_prompt(_addr(q), _addr(k), _addr(v), _addr(seq_offsets), _addr(out), int(tokens),
-                                  int(n_seqs), int(q_heads), int(kv_heads), int(head_dim), int(q_stride),
-                                  int(k_stride), int(v_stride), int(out_stride), float(scale), _stream(stream)),
-           "qmm_attn_prompt")
+    status = load().qmm_call_words(3, _PROMPT_WORDS(_word(q), _word(k), _word(v), _word(seq_offsets), _word(out),
+                                                    tokens, n_seqs, q_heads, kv_heads, head_dim, q_stride, k_stride,
+                                                    v_stride, out_stride, scale, _stream(stream)))
+    if status != QMM_OK:
+        _check(status, "qmm_attn_prompt")
 
 
 def qmm_unpack(w_packed, codes, n, k, bits, stream=None) -> None:

@@ -5,7 +5,9 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <climits>
 #include <cmath>
+#include <cstring>
 
 #include "layer_kernels.h"
 
@@ -157,6 +159,22 @@ qmm_status check_attn_cache(const qmm_kv_cache* c, bool arrays, int64_t n_seqs, 
           q_len, q_heads);
     return QMM_OK;
 }
+
+// Arguments of qmm_call_words.
+struct Words {
+    int64_t w[24];
+    // What no int holds becomes one that every check refuses.
+    int i(int k) const { return w[k] > INT_MAX ? INT_MAX : w[k] < INT_MIN ? INT_MIN : (int)w[k]; }
+    float f(int k) const {
+        double d;
+        std::memcpy(&d, &w[k], 8);
+        return (float)d;
+    }
+    template <class T = void>
+    T* p(int k) const {
+        return reinterpret_cast<T*>(w[k]);
+    }
+};
 
 }  // namespace
 
@@ -343,6 +361,32 @@ qmm_status qmm_attn_prompt(const void* q, const void* k, const void* v, const in
     PromptArgs a{q, k, v, out, seq_offsets, tokens, n_seqs, q_stride, k_stride, v_stride, out_stride, q_heads, kv_heads,
                  head_dim, scale, cus};
     return launched(launch_attn_prompt(a, static_cast<hipStream_t>(stream)), "qmm_attn_prompt");
+}
+
+qmm_status qmm_call_words(int call, const void* words) {
+    CHECK(words, QMM_ERR_INVALID_ARGUMENT, "NULL words");
+    Words a;
+    switch (call) {
+        case QMM_CALL_NORM_RESIDUAL:
+            std::memcpy(a.w, words, 15 * 8);
+            return qmm_norm_residual(a.p(0), a.i(1), a.w[2], a.p<float>(3), a.p<float>(4), a.w[5], a.f(6), a.p<float>(7),
+                                     a.p<float>(8), a.p<float>(9), a.p(10), a.w[11], a.w[12], a.f(13), a.p(14));
+        case QMM_CALL_KV_APPEND:
+            std::memcpy(a.w, words, 23 * 8);
+            return qmm_kv_append(a.p<qmm_kv_cache>(0), a.p(1), a.p(2), a.p(3), a.i(4), a.w[5], a.w[6], a.w[7],
+                                 a.p<float>(8), a.p<float>(9), a.f(10), a.p<float>(11), a.i(12), a.i(13),
+                                 a.p<int32_t>(14), a.p<int64_t>(15), a.p(16), a.p(17), a.p(18), a.i(19), a.w[20],
+                                 a.i(21), a.p(22));
+        case QMM_CALL_ATTN_CACHE:
+            std::memcpy(a.w, words, 14 * 8);
+            return qmm_attn_cache(a.p<qmm_kv_cache>(0), a.p(1), a.p<int32_t>(2), a.w[3], a.p<int32_t>(4), a.w[5], a.p(6),
+                                  a.w[7], a.i(8), a.i(9), a.f(10), a.p(11), (size_t)a.w[12], a.p(13));
+        case QMM_CALL_ATTN_PROMPT:
+            std::memcpy(a.w, words, 16 * 8);
+            return qmm_attn_prompt(a.p(0), a.p(1), a.p(2), a.p<int32_t>(3), a.p(4), a.w[5], a.w[6], a.i(7), a.i(8), a.i(9),
+                                   a.w[10], a.w[11], a.w[12], a.w[13], a.f(14), a.p(15));
+    }
+    return report(QMM_ERR_INVALID_ARGUMENT, "call=%d is none of QMM_CALL_*", call);
 }
 
 }  // extern "C"

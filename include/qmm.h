@@ -468,6 +468,14 @@ QMM_API qmm_status qmm_attn_prompt(const void *q, const void *k, const void *v,
                                    int64_t q_stride, int64_t k_stride, int64_t v_stride,
                                    int64_t out_stride, float scale, void *stream);
 
+/* One of the four calls above with its arguments as 64-bit words in their order
+ * (pointers and whole numbers as int64, float as double): for bindings in
+ * which every argument of a foreign call costs time.  Same checks, same errors.
+ * Words per call: 15, 23, 14 and 16.                                        */
+enum { QMM_CALL_NORM_RESIDUAL = 0, QMM_CALL_KV_APPEND = 1, QMM_CALL_ATTN_CACHE = 2, QMM_CALL_ATTN_PROMPT = 3 };
+
+QMM_API qmm_status qmm_call_words(int call, const void *words);
+
 /* Codes as bytes: codes[n][k] = q[n][k] (uint8).  Bit-exact view of the
  * packed format, used to check the GPU's bit extraction.                   */
 QMM_API qmm_status qmm_unpack(const void *w_packed, uint8_t *codes, int64_t n, int64_t k,

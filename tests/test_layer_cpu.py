@@ -190,3 +190,14 @@ def test_oracle_norm_of_known_rows():
     r = np.sqrt(12.5)
     assert np.allclose(u, [[3 / r, 8 / r]]) and np.allclose(h, [[1 + 6 / r, 1 + 16 / r]])
     assert np.allclose((x ** 2).mean(-1), 1)
+
+
+def test_words_that_no_int_holds_are_refused_and_no_call_is_unknown(lib):
+    # Arguments travel as 64-bit words: 2^32 + 1 must not become 1.
+    cache = qmm.KvCache(4096, 4096, 4096, 4096, 4096, 4096, 1, 1, 64, 16, 4, 32)
+    for q_len in (2 ** 32 + 1, -2 ** 32 + 1):
+        with pytest.raises(qmm.QmmError, match="q_len"):
+            qmm.qmm_attn_cache(cache, 4096, 4096, 1, 4096, 16, 4096, 1, q_len, 1, 1.0, stream=0)
+    assert lib.qmm_call_words(4, bytes(23 * 8)) == qmm.QMM_ERR_INVALID_ARGUMENT
+    assert lib.qmm_call_words(-1, bytes(23 * 8)) == qmm.QMM_ERR_INVALID_ARGUMENT
+    assert lib.qmm_call_words(0, None) == qmm.QMM_ERR_INVALID_ARGUMENT
