@@ -385,18 +385,22 @@ hipError_t launch(const PromptArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Work-groups of 128 rows where they fill the device, else of 64 with two
-// waves for every 32 rows, which halves the longest chain of steps (2048
-// tokens, 16 heads of 128: 44 us against 57; 512 tokens, 32 heads of 64: 12.2
-// against 15.0; 4 x 4096 tokens, 16 heads of 128 the other way: 418 against
-// 330).  Tiles of 32 keys let three work-groups share a compute unit at head
-// size 128 (8192 tokens, 32 heads: 558 us against 594 with 64 keys and two);
-// at 64 four fit either way, and fewer meetings win (343 us against 350, 9
-// packed prompts of up to 700 tokens 33.2 against 34.6).
+// Work-groups of 128 rows where there are two and a half or more for every
+// compute unit, else of 64 with two waves for every 32 rows, which halves the
+// longest chain of steps.  One prompt of 1500, 2048 and 3000 tokens, 32 heads of
+// 64 (1.5, 2 and 3 work-groups of 128 rows per unit): 24.6, 34.6 and 64.6 us
+// with 64 rows, 30.4, 40.7 and 61.4 with 128; of 128: 36.7, 57.9 and 112 against
+// 41.9, 59.7 and 98; 16 heads of 128, 3000 tokens (1.5): 60 against 77.  Four
+// waves for 32 rows gain 10 % at 512 and 1024 tokens and lose 20 % at 128.
+//
+// Tiles of 32 keys let three work-groups share a compute unit at head size 128
+// (8192 tokens, 32 heads: 558 us against 594 with 64 keys and two); at 64
+// four fit either way, and fewer meetings win (343 us against 350, 9 packed
+// prompts of up to 700 tokens 33.2 against 34.6).
 template <int D>
 hipError_t launch_rows(const PromptArgs& a, hipStream_t st) {
     const int64_t blocks = (a.tokens + 127) / 128 * a.q_heads;
-    if (blocks * 2 < 3 * (int64_t)a.cus && a.tokens <= 65535 * 64) return launch<D, 2, 2, 64>(a, st);
+    if (blocks * 2 < 5 * (int64_t)a.cus && a.tokens <= 65535 * 64) return launch<D, 2, 2, 64>(a, st);
     return launch<D, 4, 1, D == 128 ? 32 : 64>(a, st);
 }
 
