@@ -390,6 +390,16 @@ def _word(v):
         return v  # an address
 
 
+_CachePointer = ctypes.POINTER(KvCache)
+
+
+def _cache_word(cache):
+    """Address of the struct (0 for None): a KvCache, or what ctypes takes where a pointer to one is declared."""
+    if isinstance(cache, KvCache):
+        return ctypes.addressof(cache)
+    return ctypes.cast(_CachePointer.from_param(cache), ctypes.c_void_p).value or 0
+
+
 def qmm_norm_residual(y, y_fp16, y_stride, post_weight, gate, gate_stride, scale, residual, h, pre_weight, x, rows, n,
                       eps, stream=None) -> None:
     """h = residual + scale * gate * rmsnorm(y); x = fp16(rmsnorm(h)); asynchronous."""
@@ -403,12 +413,11 @@ def qmm_norm_residual(y, y_fp16, y_stride, post_weight, gate, gate_stride, scale
 def qmm_kv_append(cache, q, k, v, in_fp16, q_stride, k_stride, v_stride, q_norm, k_norm, eps, inv_freq, rot_dim,
                   interleaved, positions, slots, q_out, k_out, v_out, out_cached, tokens, q_heads, stream=None) -> None:
     """Rotated queries, and keys and values into the cache's slots (``cache``: a ``KvCache``); asynchronous."""
-    status = load().qmm_call_words(1, _APPEND_WORDS(ctypes.addressof(cache) if cache is not None else 0, _word(q),
-                                                    _word(k), _word(v), in_fp16, q_stride, k_stride, v_stride,
-                                                    _word(q_norm), _word(k_norm), eps, _word(inv_freq), rot_dim,
-                                                    interleaved, _word(positions), _word(slots), _word(q_out),
-                                                    _word(k_out), _word(v_out), out_cached, tokens, q_heads,
-                                                    _stream(stream)))
+    status = load().qmm_call_words(1, _APPEND_WORDS(_cache_word(cache), _word(q), _word(k), _word(v), in_fp16, q_stride,
+                                                    k_stride, v_stride, _word(q_norm), _word(k_norm), eps,
+                                                    _word(inv_freq), rot_dim, interleaved, _word(positions),
+                                                    _word(slots), _word(q_out), _word(k_out), _word(v_out), out_cached,
+                                                    tokens, q_heads, _stream(stream)))
     if status != QMM_OK:
         _check(status, "qmm_kv_append")
 
@@ -416,10 +425,9 @@ def qmm_kv_append(cache, q, k, v, in_fp16, q_stride, k_stride, v_stride, q_norm,
 def qmm_attn_cache(cache, q, page_table, table_stride, kv_lens, max_kv_len, out, n_seqs, q_len, q_heads, scale,
                    workspace=None, workspace_bytes=0, stream=None) -> None:
     """Attention of each sequence's newest ``q_len`` tokens over its cached rows; asynchronous."""
-    status = load().qmm_call_words(2, _CACHE_WORDS(ctypes.addressof(cache) if cache is not None else 0, _word(q),
-                                                   _word(page_table), table_stride, _word(kv_lens), max_kv_len,
-                                                   _word(out), n_seqs, q_len, q_heads, scale, _word(workspace),
-                                                   workspace_bytes, _stream(stream)))
+    status = load().qmm_call_words(2, _CACHE_WORDS(_cache_word(cache), _word(q), _word(page_table), table_stride,
+                                                   _word(kv_lens), max_kv_len, _word(out), n_seqs, q_len, q_heads,
+                                                   scale, _word(workspace), workspace_bytes, _stream(stream)))
     if status != QMM_OK:
         _check(status, "qmm_attn_cache")
 
