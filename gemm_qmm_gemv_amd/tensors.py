@@ -150,13 +150,22 @@ def _rows(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else dense
 
 
+def _gate_rows(gate: torch.Tensor | None, rows: int, n: int) -> int:
+    """Elements between the gate rows of neighbouring rows, 0: one row for all."""
+    if gate is None:
+        return 0
+    if gate.shape[-1:] != (n,) or (gate.numel() != n and (gate.dim() != 2 or gate.shape[0] < rows)):
+        raise ValueError("a gate of shape %s for %d rows of %d" % (tuple(gate.shape), rows, n))
+    return 0 if gate.numel() == n else _rows(gate)
+
+
 def norm_residual(y: torch.Tensor | None, residual: torch.Tensor | None, pre: torch.Tensor | None, eps: float = 1e-6,
                   post: torch.Tensor | None = None, gate: torch.Tensor | None = None, scale: float = 1.0,
                   h: torch.Tensor | None = None, x: torch.Tensor | None = None, stream=None):
     """(h, x): h = residual + scale * gate * rmsnorm(y), x = fp16(rmsnorm(h) * pre), in one launch.
 
     y fp32 or fp16 rows (a column range of a wider tensor will do), None: h is
-    the residual as it is; post None: y without a norm; gate [n] or [rows, n];
+    the residual as it is; post None: y without a norm; gate [n], [1, n] or [rows, n];
     h may be the residual (updated in place)."""
     like = residual if y is None else y
     rows, n = like.shape
@@ -167,8 +176,8 @@ def norm_residual(y: torch.Tensor | None, residual: torch.Tensor | None, pre: to
     if x is None:
         x = torch.empty((rows, n), dtype=torch.float16, device=like.device)
     qmm_norm_residual(y, y is not None and y.dtype == torch.float16, 0 if y is None else _rows(y), post, gate,
-                      _rows(gate) if gate is not None and gate.dim() == 2 else 0, scale, residual,
-                      None if y is None else h, pre, x, rows, n, eps, stream=stream)
+                      0 if y is None else _gate_rows(gate, rows, n), scale, residual, None if y is None else h, pre, x, rows, n,
+                      eps, stream=stream)
     return h, x
 
 
