@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 
 import numpy as np
 import torch
@@ -150,13 +151,35 @@ def _rows(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else dense
 
 
+def _dense(name: str, t: torch.Tensor | None, dtype: torch.dtype, *shape: int) -> None:
+    """Refuses what the kernels, which go by addresses, would take for something else: another type, gaps between
+    elements, a last axis of another length, fewer rows than `shape` has."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError("%s is %s, not %s" % (name, t.dtype, dtype))
+    if not t.is_contiguous() or t.shape[-1:] != shape[-1:] or t.numel() < math.prod(shape):
+        raise ValueError("%s of shape %s and strides %s is not dense or not %s"
+                         % (name, tuple(t.shape), t.stride(), list(shape)))
+
+
+def _floating(name: str, t: torch.Tensor | None) -> None:
+    if t is not None and t.dtype not in (torch.float16, torch.float32):
+        raise ValueError("%s is %s, neither fp16 nor fp32" % (name, t.dtype))
+
+
 def _gate_rows(gate: torch.Tensor | None, rows: int, n: int) -> int:
     """Elements between the gate rows of neighbouring rows, 0: one row for all."""
     if gate is None:
         return 0
     if gate.shape[-1:] != (n,) or (gate.numel() != n and (gate.dim() != 2 or gate.shape[0] < rows)):
         raise ValueError("a gate of shape %s for %d rows of %d" % (tuple(gate.shape), rows, n))
-    return 0 if gate.numel() == n else _rows(gate)
+    if gate.numel() == n:
+        _dense("gate", gate, torch.float32, n)
+        return 0
+    if gate.dtype != torch.float32:
+        raise ValueError("gate is %s, not fp32" % gate.dtype)
+    return _rows(gate)
 
 
 def norm_residual(y: torch.Tensor | None, residual: torch.Tensor | None, pre: torch.Tensor | None, eps: float = 1e-6,
@@ -175,6 +198,12 @@ def norm_residual(y: torch.Tensor | None, residual: torch.Tensor | None, pre: to
         h = torch.empty((rows, n), dtype=torch.float32, device=y.device)
     if x is None:
         x = torch.empty((rows, n), dtype=torch.float16, device=like.device)
+    _floating("y", y)
+    _dense("residual", residual, torch.float32, rows, n)
+    _dense("h", h, torch.float32, rows, n)
+    _dense("x", x, torch.float16, rows, n)
+    _dense("post", post, torch.float32, n)
+    _dense("pre", pre, torch.float32, n)
     qmm_norm_residual(y, y is not None and y.dtype == torch.float16, 0 if y is None else _rows(y), post, gate,
                       0 if y is None else _gate_rows(gate, rows, n), scale, residual, None if y is None else h, pre, x, rows, n,
                       eps, stream=stream)

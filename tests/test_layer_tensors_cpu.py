@@ -39,3 +39,35 @@ def test_gates_of_another_shape_are_refused(calls, gate):
     with pytest.raises(ValueError, match="gate"):
         norm(gate=gate)
     assert not calls
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=torch.zeros(3, 96)[:, 8:72]), dict(y=torch.zeros(3, 64, dtype=F16)), dict(y=None), dict(residual=None),
+    dict(residual=torch.zeros(1, 3, 64)), dict(h=torch.zeros(8, 64)), dict(x=torch.zeros(3, 64, dtype=F16)), dict(pre=None),
+    dict(pre=torch.zeros(1, 64), post=torch.zeros(64)),
+])
+def test_operands_of_the_norm(calls, kw):
+    norm(**kw)
+    assert len(calls) == 1
+
+
+@pytest.mark.parametrize("name,t", [
+    ("y", torch.zeros(3, 64, dtype=torch.bfloat16)), ("y", torch.zeros(3, 64, dtype=torch.float64)),
+    ("residual", torch.zeros(3, 64, dtype=F16)), ("residual", torch.zeros(3, 80)[:, :64]), ("residual", torch.zeros(2, 64)),
+    ("residual", torch.zeros(3, 65)), ("residual", torch.zeros(1, 64).expand(3, 64)), ("h", torch.zeros(3, 64, dtype=torch.float64)),
+    ("h", torch.zeros(3, 80)[:, :64]), ("h", torch.zeros(64, 3).t()), ("x", torch.zeros(3, 64)),
+    ("x", torch.zeros(3, 80, dtype=F16)[:, :64]), ("x", torch.zeros(2, 64, dtype=F16)), ("pre", torch.zeros(64, dtype=F16)),
+    ("pre", torch.zeros(63)), ("pre", torch.zeros(128)[::2]), ("post", torch.zeros(64, dtype=F16)), ("post", torch.zeros(1)),
+    ("gate", torch.zeros(64, dtype=F16)), ("gate", torch.zeros(3, 64, dtype=F16)), ("gate", torch.zeros(128)[::2]),
+])
+def test_operands_that_the_norm_would_misread_are_refused(calls, name, t):
+    with pytest.raises(ValueError, match=name):
+        norm(**{name: t})
+    assert not calls
+
+
+def test_a_residual_alone_is_looked_at_too(calls):
+    for t in (torch.zeros(3, 64, dtype=F16), torch.zeros(3, 80)[:, :64]):
+        with pytest.raises(ValueError, match="residual"):
+            norm(y=None, residual=t)
+    assert not calls
