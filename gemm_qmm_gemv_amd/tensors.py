@@ -163,6 +163,17 @@ def _dense(name: str, t: torch.Tensor | None, dtype: torch.dtype, *shape: int) -
                          % (name, tuple(t.shape), t.stride(), list(shape)))
 
 
+def _vector(name: str, t: torch.Tensor | None, dtype: torch.dtype, size: int) -> None:
+    """The same for `size` neighbouring values or more."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError("%s is %s, not %s" % (name, t.dtype, dtype))
+    if not t.is_contiguous() or t.numel() < size:
+        raise ValueError("%s of shape %s and strides %s is not dense or below %d values"
+                         % (name, tuple(t.shape), t.stride(), size))
+
+
 def _floating(name: str, t: torch.Tensor | None) -> None:
     if t is not None and t.dtype not in (torch.float16, torch.float32):
         raise ValueError("%s is %s, neither fp16 nor fp32" % (name, t.dtype))
@@ -229,8 +240,8 @@ def kv_append(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
               q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None, eps: float = 1e-6,
               out: torch.Tensor | None = None, prompt_rows: bool = False, cached_values: bool = False, stream=None):
     """New tokens' rows q, k and v [tokens, heads * head_dim] (column ranges of one fused product will do): returns the
-    normed and rotated queries [tokens, q_heads, head_dim] and stores keys and values in `slots`.  With prompt_rows it
-    returns (q, k, v) for attn_prompt, k and v as the cache stands for them if cached_values."""
+    normed and rotated queries [tokens, q_heads, head_dim] and stores keys and values in `slots` (int64; positions int32).
+    With prompt_rows it returns (q, k, v) for attn_prompt, k and v as the cache stands for them if cached_values."""
     tokens, d = q.shape[0], cache.head_dim
     q_heads = q[0].numel() // d if tokens else q.shape[-1] // d
     assert q.dtype == k.dtype == v.dtype
@@ -240,6 +251,9 @@ def kv_append(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if prompt_rows:
         k_out = torch.empty((tokens, cache.kv_heads, d), dtype=torch.float16, device=q.device)
         v_out = torch.empty_like(k_out)
+    if inv_freq is not None:
+        _vector("positions", positions, torch.int32, tokens)
+    _vector("slots", slots, torch.int64, tokens)
     qmm_kv_append(cache, q, k, v, q.dtype == torch.float16, _rows(q), _rows(k), _rows(v), q_norm, k_norm, eps,
                   inv_freq, 0 if inv_freq is None else 2 * inv_freq.numel(), interleaved, positions, slots, out,
                   k_out, v_out, cached_values, tokens, q_heads, stream=stream)
@@ -258,8 +272,12 @@ def attn_workspace(cache: KvCache, n_seqs: int, q_len: int, q_heads: int, max_kv
 def attn_cache(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, max_kv_len: int,
                scale: float | None = None, q_len: int = 1, out: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """Attention of q [n_seqs * q_len, q_heads, head_dim], each sequence's newest q_len tokens, over the cache."""
+    """Attention of q [n_seqs * q_len, q_heads, head_dim], each sequence's newest q_len tokens, over the cache
+    (page_table [n_seqs, pages of a sequence] and kv_lens [n_seqs] int32)."""
     n_seqs, q_heads = kv_lens.shape[0], q.shape[-2]
+    _vector("kv_lens", kv_lens, torch.int32, n_seqs)
+    if page_table.dtype != torch.int32:
+        raise ValueError("page_table is %s, not torch.int32" % page_table.dtype)
     assert q.is_contiguous() and q.numel() == n_seqs * q_len * q_heads * cache.head_dim
     if out is None:
         out = torch.empty_like(q)
@@ -275,8 +293,10 @@ def attn_cache(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_len
 
 def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_offsets: torch.Tensor,
                 scale: float | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """Causal attention in each of the sequences packed in q [tokens, q_heads, d], k and v [tokens, kv_heads, d]."""
+    """Causal attention in each of the sequences packed in q [tokens, q_heads, d], k and v [tokens, kv_heads, d]
+    (seq_offsets [sequences + 1] int32)."""
     tokens, q_heads, d = q.shape
+    _vector("seq_offsets", seq_offsets, torch.int32, 1)
     if out is None:
         out = torch.empty((tokens, q_heads, d), dtype=torch.float16, device=q.device)
     qmm_attn_prompt(q, k, v, seq_offsets, out, tokens, seq_offsets.numel() - 1, q_heads, k.shape[1], d, _rows(q),

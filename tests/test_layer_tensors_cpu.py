@@ -71,3 +71,56 @@ def test_a_residual_alone_is_looked_at_too(calls):
         with pytest.raises(ValueError, match="residual"):
             norm(y=None, residual=t)
     assert not calls
+
+
+def cache(bits=4, group=32, pages=4, hkv=2, d=64, page=16):
+    return tensors.kv_cache(pages, hkv, d, page, bits, group, device="cpu")
+
+
+def append(tokens=3, hq=4, hkv=2, d=64, **kw):
+    a = dict(cache=cache(hkv=hkv, d=d), q=torch.zeros(tokens, hq * d, dtype=F16), k=torch.zeros(tokens, hkv * d, dtype=F16),
+             v=torch.zeros(tokens, hkv * d, dtype=F16), positions=torch.zeros(tokens, dtype=I32), slots=torch.zeros(tokens, dtype=I64),
+             inv_freq=torch.zeros(d // 2))
+    a.update(kw)
+    return tensors.kv_append(**a)
+
+
+def attend(n=3, q_len=2, hq=4, hkv=2, d=64, **kw):
+    a = dict(cache=cache(hkv=hkv, d=d), q=torch.zeros(n * q_len, hq, d, dtype=F16), page_table=torch.zeros(n, 4, dtype=I32),
+             kv_lens=torch.zeros(n, dtype=I32), max_kv_len=64, q_len=q_len, workspace=torch.zeros(16, dtype=torch.uint8))
+    a.update(kw)
+    return tensors.attn_cache(**a)
+
+
+def prompt(tokens=10, hq=4, hkv=2, d=64, **kw):
+    a = dict(q=torch.zeros(tokens, hq, d, dtype=F16), k=torch.zeros(tokens, hkv, d, dtype=F16),
+             v=torch.zeros(tokens, hkv, d, dtype=F16), seq_offsets=torch.tensor([0, 4, 10], dtype=I32))
+    a.update(kw)
+    return tensors.attn_prompt(**a)
+
+
+@pytest.mark.parametrize("call,name,t", [
+    (append, "positions", torch.zeros(3, dtype=I64)), (append, "positions", torch.zeros(3)), (append, "positions", torch.zeros(2, dtype=I32)),
+    (append, "positions", torch.zeros(6, dtype=I32)[::2]), (append, "slots", torch.zeros(3, dtype=I32)),
+    (append, "slots", torch.zeros(2, dtype=I64)), (append, "slots", torch.zeros(1, dtype=I64).expand(3)),
+    (append, "slots", torch.zeros(6, dtype=I64)[::2]), (attend, "kv_lens", torch.zeros(3, dtype=I64)),
+    (attend, "kv_lens", torch.zeros(6, dtype=I32)[::2]), (attend, "page_table", torch.zeros(3, 4, dtype=I64)),
+    (attend, "page_table", torch.zeros(3, 4, dtype=torch.int16)), (prompt, "seq_offsets", torch.tensor([0, 4, 10])),
+    (prompt, "seq_offsets", torch.zeros(6, dtype=I32)[::2]), (prompt, "seq_offsets", torch.zeros(0, dtype=I32)),
+])
+def test_indices_of_another_type_or_with_gaps_are_refused(calls, call, name, t):
+    with pytest.raises(ValueError, match=name):
+        call(**{name: t})
+    assert not calls
+
+
+@pytest.mark.parametrize("call,kw", [
+    (append, {}), (append, dict(positions=torch.zeros(9, dtype=I32), slots=torch.zeros(9, dtype=I64))), (append, dict(slots=None)),
+    (append, dict(positions=None, inv_freq=None)), (append, dict(positions=torch.zeros(3, dtype=I64), inv_freq=None)),
+    (append, dict(tokens=0)), (attend, {}), (attend, dict(n=1)), (attend, dict(page_table=torch.zeros(3, 9, dtype=I32)[:, 2:6])),
+    (attend, dict(n=0)), (prompt, {}), (prompt, dict(seq_offsets=torch.tensor([0], dtype=I32))),
+    (prompt, dict(tokens=0, seq_offsets=torch.tensor([0, 0], dtype=I32))),
+])
+def test_calls_that_are_handed_on(calls, call, kw):
+    call(**kw)
+    assert len(calls) == 1
