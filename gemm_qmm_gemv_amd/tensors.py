@@ -278,6 +278,12 @@ def attn_cache(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_len
     _vector("kv_lens", kv_lens, torch.int32, n_seqs)
     if page_table.dtype != torch.int32:
         raise ValueError("page_table is %s, not torch.int32" % page_table.dtype)
+    if page_table.dim() != 2 or page_table.shape[0] < n_seqs or (page_table.shape[1] > 1 and page_table.stride(1) != 1) \
+            or page_table.shape[1] * cache.page_size < max_kv_len:
+        raise ValueError("a page_table of shape %s and strides %s for %d sequences of up to %d rows"
+                         % (tuple(page_table.shape), page_table.stride(), n_seqs, max_kv_len))
+    _dense("q", q, torch.float16, n_seqs * q_len * q_heads, cache.head_dim)
+    _vector("out", out, torch.float16, q.numel())
     assert q.is_contiguous() and q.numel() == n_seqs * q_len * q_heads * cache.head_dim
     if out is None:
         out = torch.empty_like(q)
@@ -285,6 +291,8 @@ def attn_cache(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_len
         # Made and given back on the current stream.
         assert stream is None, "a call on another stream needs a workspace of its own"
         workspace = attn_workspace(cache, n_seqs, q_len, q_heads, max_kv_len, q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace is not dense")
     qmm_attn_cache(cache, q, page_table, page_table.stride(0) if n_seqs > 1 else page_table.shape[1], kv_lens,
                    max_kv_len, out, n_seqs, q_len, q_heads, cache.head_dim ** -0.5 if scale is None else scale,
                    workspace, workspace.numel() * workspace.element_size(), stream=stream)
@@ -297,6 +305,14 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_offsets: 
     (seq_offsets [sequences + 1] int32)."""
     tokens, q_heads, d = q.shape
     _vector("seq_offsets", seq_offsets, torch.int32, 1)
+    for name, t, row in (("q", q, (q_heads, d)), ("k", k, (k.shape[1], d)), ("v", v, (k.shape[1], d)), ("out", out, (q_heads * d,))):
+        if t is None:
+            continue
+        if t.dtype != torch.float16:
+            raise ValueError("%s is %s, not fp16" % (name, t.dtype))
+        got = t.shape[1:] if name != "out" else (math.prod(t.shape[1:]),)
+        if t.shape[0] < tokens or got != row:
+            raise ValueError("%s of shape %s for %d tokens of %s values" % (name, tuple(t.shape), tokens, row))
     if out is None:
         out = torch.empty((tokens, q_heads, d), dtype=torch.float16, device=q.device)
     qmm_attn_prompt(q, k, v, seq_offsets, out, tokens, seq_offsets.numel() - 1, q_heads, k.shape[1], d, _rows(q),

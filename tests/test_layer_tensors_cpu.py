@@ -124,3 +124,34 @@ def test_indices_of_another_type_or_with_gaps_are_refused(calls, call, name, t):
 def test_calls_that_are_handed_on(calls, call, kw):
     call(**kw)
     assert len(calls) == 1
+
+
+@pytest.mark.parametrize("call,name,t", [
+    (attend, "q", torch.zeros(6, 4, 64)), (attend, "q", torch.zeros(6, 2, 128, dtype=F16)), (attend, "out", torch.zeros(6, 4, 64)),
+    (attend, "out", torch.zeros(6, 8, 64, dtype=F16)[:, :4]), (attend, "out", torch.zeros(5, 4, 64, dtype=F16)),
+    (attend, "page_table", torch.zeros(4, 3, dtype=I32).t()), (attend, "page_table", torch.zeros(3, 8, dtype=I32)[:, ::2]),
+    (attend, "page_table", torch.zeros(2, 4, dtype=I32)), (attend, "page_table", torch.zeros(4, dtype=I32)),
+    # Rows are wide enough, but not what belongs to a sequence.
+    (attend, "page_table", torch.zeros(3, 8, dtype=I32)[:, 5:]), (attend, "workspace", torch.zeros(64, dtype=torch.uint8)[::2]),
+    (prompt, "q", torch.zeros(10, 4, 64)), (prompt, "k", torch.zeros(10, 2, 64)), (prompt, "v", torch.zeros(10, 2, 64, dtype=torch.bfloat16)),
+    (prompt, "k", torch.zeros(9, 2, 64, dtype=F16)), (prompt, "v", torch.zeros(9, 2, 64, dtype=F16)),
+    (prompt, "v", torch.zeros(10, 1, 64, dtype=F16)), (prompt, "k", torch.zeros(10, 2, 128, dtype=F16)),
+    (prompt, "v", torch.zeros(10, 4, 32, dtype=F16)), (prompt, "out", torch.zeros(10, 4, 64)),
+    (prompt, "out", torch.zeros(9, 4, 64, dtype=F16)), (prompt, "out", torch.zeros(10, 4, 32, dtype=F16)),
+])
+def test_operands_that_attention_would_misread_are_refused(calls, call, name, t):
+    with pytest.raises(ValueError, match=name):
+        call(**{name: t})
+    assert not calls
+
+
+@pytest.mark.parametrize("call,kw", [
+    (attend, dict(out=torch.zeros(6, 4 * 64, dtype=F16))), (attend, dict(q=torch.zeros(3, 2, 4, 64, dtype=F16))),
+    (attend, dict(page_table=torch.zeros(5, 4, dtype=I32))), (attend, dict(page_table=torch.zeros(3, 1, dtype=I32), max_kv_len=16)),
+    (prompt, dict(out=torch.zeros(10, 4 * 64, dtype=F16))), (prompt, dict(out=torch.zeros(10, 4 * 64 + 8, dtype=F16)[:, :256])),
+    (prompt, dict(k=torch.zeros(16, 2, 64, dtype=F16), v=torch.zeros(16, 2, 64, dtype=F16))),
+    (prompt, dict(k=torch.zeros(10, 8, 64, dtype=F16)[:, 2:4])),
+])
+def test_other_layouts_of_attention_are_handed_on(calls, call, kw):
+    call(**kw)
+    assert len(calls) == 1
