@@ -243,8 +243,17 @@ def kv_append(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     normed and rotated queries [tokens, q_heads, head_dim] and stores keys and values in `slots` (int64; positions int32).
     With prompt_rows it returns (q, k, v) for attn_prompt, k and v as the cache stands for them if cached_values."""
     tokens, d = q.shape[0], cache.head_dim
-    q_heads = q[0].numel() // d if tokens else q.shape[-1] // d
+    width = math.prod(q.shape[1:])
+    q_heads = width // d
+    _floating("q", q)
     assert q.dtype == k.dtype == v.dtype
+    for name, t, heads in (("q", q, q_heads), ("k", k, cache.kv_heads), ("v", v, cache.kv_heads)):
+        if t.shape[0] < tokens or math.prod(t.shape[1:]) != heads * d:
+            raise ValueError("%s of shape %s for %d tokens of %d heads of %d" % (name, tuple(t.shape), tokens, heads, d))
+    _vector("out", out, torch.float16, tokens * width)
+    _vector("inv_freq", inv_freq, torch.float32, 0)
+    _vector("q_norm", q_norm, torch.float32, d)
+    _vector("k_norm", k_norm, torch.float32, d)
     if out is None:
         out = torch.empty((tokens, q_heads, d), dtype=torch.float16, device=q.device)
     k_out = v_out = None

@@ -155,3 +155,38 @@ def test_operands_that_attention_would_misread_are_refused(calls, call, name, t)
 def test_other_layouts_of_attention_are_handed_on(calls, call, kw):
     call(**kw)
     assert len(calls) == 1
+
+
+@pytest.mark.parametrize("name,t", [
+    ("q", torch.zeros(3, 260, dtype=F16)), ("k", torch.zeros(2, 128, dtype=F16)), ("k", torch.zeros(3, 64, dtype=F16)),
+    ("k", torch.zeros(3, 256, dtype=F16)), ("v", torch.zeros(3, 130, dtype=F16)), ("v", torch.zeros(1, 128, dtype=F16)),
+    ("out", torch.zeros(3, 4, 64)), ("out", torch.zeros(2, 4, 64, dtype=F16)), ("out", torch.zeros(3, 8, 64, dtype=F16)[:, :4]),
+    ("inv_freq", torch.zeros(32, dtype=torch.float64)), ("inv_freq", torch.zeros(64)[::2]), ("q_norm", torch.zeros(64, dtype=F16)),
+    ("q_norm", torch.zeros(32)), ("k_norm", torch.zeros(128)[::2]), ("k_norm", torch.zeros(64, dtype=torch.float64)),
+])
+def test_operands_that_the_append_would_misread_are_refused(calls, name, t):
+    with pytest.raises(ValueError, match=name):
+        append(**{name: t})
+    assert not calls
+
+
+def test_rows_of_bfloat16_are_refused(calls):
+    rows = {x: torch.zeros(3, w, dtype=torch.bfloat16) for x, w in (("q", 256), ("k", 128), ("v", 128))}
+    with pytest.raises(ValueError, match="q is"):
+        append(**rows)
+    assert not calls
+
+
+Q_HEADS = 21  # its place among qmm_kv_append's arguments
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=torch.zeros(3, 4, 64, dtype=F16), k=torch.zeros(3, 2, 64, dtype=F16)), dict(out=torch.zeros(3, 256, dtype=F16)),
+    dict(out=torch.zeros(9, 4, 64, dtype=F16)), dict(q_norm=torch.zeros(64), k_norm=torch.zeros(64)),
+    {x: torch.zeros(3, 512)[:, a:b] for x, a, b in (("q", 0, 256), ("k", 256, 384), ("v", 384, 512))},
+    dict(k=torch.zeros(8, 128, dtype=F16), v=torch.zeros(8, 128, dtype=F16)),
+    dict(tokens=0, q=torch.zeros(0, 4, 64, dtype=F16)),
+])
+def test_other_layouts_of_the_append_are_handed_on(calls, kw):
+    append(**kw)
+    assert len(calls) == 1 and calls[0][Q_HEADS] == 4
