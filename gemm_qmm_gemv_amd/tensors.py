@@ -151,6 +151,21 @@ def _rows(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else dense
 
 
+def _output(shape: tuple, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """A tensor that a call on `stream` writes.  On another stream than the current one it comes from that stream's
+    memory (a block of the current one may still be read by work behind which the call does not wait), and goes back
+    only when the current stream, on which the caller may use it, is done with it too."""
+    if stream is None or _stream(stream) == _stream(None):
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
 def _dense(name: str, t: torch.Tensor | None, dtype: torch.dtype, *shape: int) -> None:
     """Refuses what the kernels, which go by addresses, would take for something else: another type, gaps between
     elements, a last axis of another length, fewer rows than `shape` has."""
@@ -206,9 +221,9 @@ def norm_residual(y: torch.Tensor | None, residual: torch.Tensor | None, pre: to
     if y is None:
         h = residual
     elif h is None:
-        h = torch.empty((rows, n), dtype=torch.float32, device=y.device)
+        h = _output((rows, n), torch.float32, y.device, stream)
     if x is None:
-        x = torch.empty((rows, n), dtype=torch.float16, device=like.device)
+        x = _output((rows, n), torch.float16, like.device, stream)
     _floating("y", y)
     _dense("residual", residual, torch.float32, rows, n)
     _dense("h", h, torch.float32, rows, n)
@@ -255,11 +270,10 @@ def kv_append(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     _vector("q_norm", q_norm, torch.float32, d)
     _vector("k_norm", k_norm, torch.float32, d)
     if out is None:
-        out = torch.empty((tokens, q_heads, d), dtype=torch.float16, device=q.device)
+        out = _output((tokens, q_heads, d), torch.float16, q.device, stream)
     k_out = v_out = None
     if prompt_rows:
-        k_out = torch.empty((tokens, cache.kv_heads, d), dtype=torch.float16, device=q.device)
-        v_out = torch.empty_like(k_out)
+        k_out, v_out = (_output((tokens, cache.kv_heads, d), torch.float16, q.device, stream) for _ in range(2))
     if inv_freq is not None:
         _vector("positions", positions, torch.int32, tokens)
     _vector("slots", slots, torch.int64, tokens)
@@ -295,7 +309,7 @@ def attn_cache(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_len
     _vector("out", out, torch.float16, q.numel())
     assert q.is_contiguous() and q.numel() == n_seqs * q_len * q_heads * cache.head_dim
     if out is None:
-        out = torch.empty_like(q)
+        out = _output(tuple(q.shape), torch.float16, q.device, stream)
     if workspace is None:
         # Made and given back on the current stream.
         assert stream is None, "a call on another stream needs a workspace of its own"
@@ -323,7 +337,7 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_offsets: 
         if t.shape[0] < tokens or got != row:
             raise ValueError("%s of shape %s for %d tokens of %s values" % (name, tuple(t.shape), tokens, row))
     if out is None:
-        out = torch.empty((tokens, q_heads, d), dtype=torch.float16, device=q.device)
+        out = _output((tokens, q_heads, d), torch.float16, q.device, stream)
     qmm_attn_prompt(q, k, v, seq_offsets, out, tokens, seq_offsets.numel() - 1, q_heads, k.shape[1], d, _rows(q),
                     _rows(k), _rows(v), _rows(out), d ** -0.5 if scale is None else scale, stream=stream)
     return out
