@@ -166,6 +166,19 @@ def _output(shape: tuple, dtype: torch.dtype, device, stream) -> torch.Tensor:
     return t
 
 
+def _on_device(*ts) -> None:
+    """Refuses tensors that are not all on the current GPU, where the call is launched (addresses are not looked at)."""
+    here = None
+    for t in ts:
+        if not isinstance(t, torch.Tensor):
+            continue
+        at = t.get_device()  # -1: host memory
+        if here is None and at >= 0:
+            here = torch.cuda.current_device()
+        if at < 0 or at != here:
+            raise ValueError("a tensor is on %s, not on the current GPU" % t.device)
+
+
 def _dense(name: str, t: torch.Tensor | None, dtype: torch.dtype, *shape: int) -> None:
     """Refuses what the kernels, which go by addresses, would take for something else: another type, gaps between
     elements, a last axis of another length, fewer rows than `shape` has."""
@@ -216,6 +229,7 @@ def norm_residual(y: torch.Tensor | None, residual: torch.Tensor | None, pre: to
     y fp32 or fp16 rows (a column range of a wider tensor will do), None: h is
     the residual as it is; post None: y without a norm; gate [n], [1, n] or [rows, n];
     h may be the residual (updated in place)."""
+    _on_device(y, residual, pre, post, gate, h, x)
     like = residual if y is None else y
     rows, n = like.shape
     if y is None:
@@ -257,6 +271,7 @@ def kv_append(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """New tokens' rows q, k and v [tokens, heads * head_dim] (column ranges of one fused product will do): returns the
     normed and rotated queries [tokens, q_heads, head_dim] and stores keys and values in `slots` (int64; positions int32).
     With prompt_rows it returns (q, k, v) for attn_prompt, k and v as the cache stands for them if cached_values."""
+    _on_device(q, k, v, positions, slots, inv_freq, q_norm, k_norm, out, *getattr(cache, "keep", ()))
     tokens, d = q.shape[0], cache.head_dim
     width = math.prod(q.shape[1:])
     q_heads = width // d
@@ -297,6 +312,7 @@ def attn_cache(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_len
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Attention of q [n_seqs * q_len, q_heads, head_dim], each sequence's newest q_len tokens, over the cache
     (page_table [n_seqs, pages of a sequence] and kv_lens [n_seqs] int32)."""
+    _on_device(q, page_table, kv_lens, out, workspace, *getattr(cache, "keep", ()))
     n_seqs, q_heads = kv_lens.shape[0], q.shape[-2]
     _vector("kv_lens", kv_lens, torch.int32, n_seqs)
     if page_table.dtype != torch.int32:
@@ -326,6 +342,7 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_offsets: 
                 scale: float | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Causal attention in each of the sequences packed in q [tokens, q_heads, d], k and v [tokens, kv_heads, d]
     (seq_offsets [sequences + 1] int32)."""
+    _on_device(q, k, v, seq_offsets, out)
     tokens, q_heads, d = q.shape
     _vector("seq_offsets", seq_offsets, torch.int32, 1)
     for name, t, row in (("q", q, (q_heads, d)), ("k", k, (k.shape[1], d)), ("v", v, (k.shape[1], d)), ("out", out, (q_heads * d,))):

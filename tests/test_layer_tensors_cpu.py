@@ -9,8 +9,9 @@ F16, F32, I32, I64 = torch.float16, torch.float32, torch.int32, torch.int64
 
 @pytest.fixture
 def calls(monkeypatch):
-    """Arguments of the library's calls, which are not made."""
+    """Arguments of the library's calls, which are not made; tensors may be on the host."""
     seen = []
+    monkeypatch.setattr(tensors, "_on_device", lambda *ts: None)
     for f in ("qmm_norm_residual", "qmm_kv_append", "qmm_attn_cache", "qmm_attn_prompt"):
         monkeypatch.setattr(tensors, f, lambda *a, **kw: seen.append(a))
     return seen
@@ -190,3 +191,58 @@ Q_HEADS = 21  # its place among qmm_kv_append's arguments
 def test_other_layouts_of_the_append_are_handed_on(calls, kw):
     append(**kw)
     assert len(calls) == 1 and calls[0][Q_HEADS] == 4
+
+
+@pytest.mark.parametrize("call", [norm, append, attend, prompt])
+def test_tensors_in_host_memory_are_refused(monkeypatch, call):
+    for f in ("qmm_norm_residual", "qmm_kv_append", "qmm_attn_cache", "qmm_attn_prompt"):
+        monkeypatch.setattr(tensors, f, None)
+    with pytest.raises(ValueError, match="on cpu"):
+        call()
+
+
+def test_every_operand_is_looked_at(monkeypatch):
+    seen = []
+
+    def note(*ts):
+        seen.extend(ts)
+        raise ValueError
+    monkeypatch.setattr(tensors, "_on_device", note)
+    given = {n: torch.zeros(1) for n in ("y", "residual", "pre", "post", "gate", "h", "x")}
+    named = {n: torch.zeros(1) for n in ("q", "k", "v", "positions", "slots", "inv_freq", "q_norm", "k_norm", "out")}
+    held = cache()
+    for call, ts in ((tensors.norm_residual, given), (tensors.kv_append, named | dict(cache=held))):
+        seen.clear()
+        with pytest.raises(ValueError):
+            call(**ts)
+        for t in ts.values():
+            for u in (t.keep if t is held else (t,)):
+                assert any(u is s for s in seen)
+    named = {n: torch.zeros(1) for n in ("q", "page_table", "kv_lens", "out", "workspace")}
+    seen.clear()
+    with pytest.raises(ValueError):
+        tensors.attn_cache(held, max_kv_len=1, **named)
+    assert all(any(u is s for s in seen) for u in list(named.values()) + list(held.keep))
+    named = {n: torch.zeros(1) for n in ("q", "k", "v", "seq_offsets", "out")}
+    seen.clear()
+    with pytest.raises(ValueError):
+        tensors.attn_prompt(**named)
+    assert all(any(u is s for s in seen) for u in named.values())
+
+
+class _On:
+    """Stands in for a tensor on some device."""
+    def __init__(self, at):
+        self.at, self.device = at, "cuda:%d" % at
+
+    def get_device(self):
+        return self.at
+
+
+def test_tensors_of_another_gpu_are_refused(monkeypatch):
+    monkeypatch.setattr(torch, "Tensor", _On)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    tensors._on_device(_On(1), None, 4096, _On(1))
+    for ts in ((_On(0),), (_On(1), _On(0)), (_On(1), _On(-1)), (_On(-1), _On(1))):
+        with pytest.raises(ValueError, match="not on the current GPU"):
+            tensors._on_device(*ts)
