@@ -144,6 +144,10 @@ def unpack(dq: dict, stream=None) -> torch.Tensor:
 
 def _rows(t: torch.Tensor) -> int:
     """Elements between the token rows of t; the rest of each row is dense."""
+    if t.dim() == 2:
+        (rows, n), (step, inner) = t.shape, t.stride()
+        assert n == 1 or inner == 1, "rows must be dense"
+        return step if rows > 1 else n
     dense = 1
     for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         assert size == 1 or step == dense, "rows must be dense"
@@ -173,16 +177,16 @@ def _on_device(*ts) -> None:
         if not isinstance(t, torch.Tensor):
             continue
         at = t.get_device()  # -1: host memory
-        if here is None and at >= 0:
-            here = torch.cuda.current_device()
-        if at < 0 or at != here:
-            raise ValueError("a tensor is on %s, not on the current GPU" % t.device)
+        if at != here:
+            if at < 0 or here is not None or at != torch.cuda.current_device():
+                raise ValueError("a tensor is on %s, not on the current GPU" % t.device)
+            here = at
 
 
 def _dense(name: str, t: torch.Tensor | None, dtype: torch.dtype, *shape: int) -> None:
     """Refuses what the kernels, which go by addresses, would take for something else: another type, gaps between
     elements, a last axis of another length, fewer rows than `shape` has."""
-    if t is None:
+    if t is None or (t.dtype == dtype and t.shape == shape and t.is_contiguous()):
         return
     if t.dtype != dtype:
         raise ValueError("%s is %s, not %s" % (name, t.dtype, dtype))
@@ -278,7 +282,7 @@ def kv_append(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     _floating("q", q)
     assert q.dtype == k.dtype == v.dtype
     for name, t, heads in (("q", q, q_heads), ("k", k, cache.kv_heads), ("v", v, cache.kv_heads)):
-        if t.shape[0] < tokens or math.prod(t.shape[1:]) != heads * d:
+        if t.shape != (tokens, heads * d) and (t.shape[0] < tokens or math.prod(t.shape[1:]) != heads * d):
             raise ValueError("%s of shape %s for %d tokens of %d heads of %d" % (name, tuple(t.shape), tokens, heads, d))
     _vector("out", out, torch.float16, tokens * width)
     _vector("inv_freq", inv_freq, torch.float32, 0)
@@ -346,7 +350,7 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_offsets: 
     tokens, q_heads, d = q.shape
     _vector("seq_offsets", seq_offsets, torch.int32, 1)
     for name, t, row in (("q", q, (q_heads, d)), ("k", k, (k.shape[1], d)), ("v", v, (k.shape[1], d)), ("out", out, (q_heads * d,))):
-        if t is None:
+        if t is None or (t.dtype == torch.float16 and t.shape == (tokens, *row)):
             continue
         if t.dtype != torch.float16:
             raise ValueError("%s is %s, not fp16" % (name, t.dtype))
