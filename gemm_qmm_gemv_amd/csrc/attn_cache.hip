@@ -332,6 +332,9 @@ __device__ __forceinline__ f16x8 v_frag(const u32 (&w)[8][VW], int i, const u32x
     return frag(out[0], out[1], out[2], out[3]);
 }
 
+// Bits 15 and 31: of either half of a pair, whether its exponent is all ones
+// (an infinity or a NaN): adding one to it carries into the sign's place.
+__device__ __forceinline__ u32 carry_of_ones(u32 pair) { return (pair & 0x7C007C00u) + 0x04000400u; }
 __device__ __forceinline__ bool not_finite(u32 pair, int half) {
     return ((pair >> (16 * half)) & 0x7C00u) == 0x7C00u;
 }
@@ -519,12 +522,34 @@ __device__ __forceinline__ void attend(const CacheAttnArgs& a, const Segment& sg
             // token's row is seen by some rows only: if its values are not
             // finite they are cleared as well and the rows that see it get
             // a NaN score instead.
+            [[maybe_unused]] u32 beyond[4] = {0, 0, 0, 0};  // of cached rows 2p and 2p + 1: bits 15 and 31
+            if constexpr (C::Q) {
+                // A value leaves fp16 with a scale or min that is not finite,
+                // or with finite ones and a high code.  |scale| times the highest
+                // code plus |min|, rounded once as the values are, bounds them
+                // all, and only where that leaves fp16 are they looked at.
+                constexpr float TOP = (float)((1 << BITS) - 1);
+                u32 reach = 0;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const f16x2 sc = as_h2(r.vs[p / 2][p % 2] & 0x7FFF7FFFu), mn = as_h2(r.vm[p / 2][p % 2] & 0x7FFF7FFFu);
+                    reach |= carry_of_ones(as_u32(__builtin_elementwise_fma(sc, f16x2{(f16)TOP, (f16)TOP}, mn)));
+                }
+                if (__any(reach & 0x80008000u)) {
+#pragma unroll
+                    for (int i = 0; i < VC; ++i) {
+                        const u32x4 w = __builtin_bit_cast(u32x4, v_frag<BITS>(r.v, i, r.vs, r.vm));
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) beyond[p] |= carry_of_ones(w[p]);
+                    }
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int t = first + 16 * (j / 4) + 4 * g + j % 4;
                 bool odd = false;
                 if constexpr (C::Q) {
-                    odd = not_finite(r.vs[j / 4][j % 4 / 2], j % 2) || not_finite(r.vm[j / 4][j % 4 / 2], j % 2);
+                    odd = (beyond[j / 2] & (j % 2 ? 0x80000000u : 0x8000u)) != 0;
                 } else {
 #pragma unroll
                     for (int w = 0; w < C::VW; ++w) odd = odd || not_finite(r.v[j][w], 0) || not_finite(r.v[j][w], 1);
