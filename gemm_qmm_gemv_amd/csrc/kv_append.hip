@@ -7,8 +7,8 @@
 //     (a, b) -> (a cos t - b sin t, b cos t + a sin t),
 //     a, b = elements i and i + rot/2 (or 2i and 2i + 1, interleaved)
 //   group of `group` neighbours of a row, b bits:
-//     m = fp16(min), s = fp16((max - min) / (2^b - 1)),
-//     code = round((x - m) / s) clamped to [0, 2^b - 1]  (0 where s = 0)
+//     m = fp16(min), s = fp16((max - min) / (2^b - 1))  (NaN where m is infinite),
+//     code = round((x - m) / s) clamped to [0, 2^b - 1]  (0 where s = 0 or not finite)
 //
 // Bound by memory, and into 4 bits by the vector units as well (90 % busy with
 // 4096 tokens of 48 heads of 64).  A lane holds 8 neighbours of a row, so D/8 lanes make a
@@ -237,8 +237,13 @@ __global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a, int tile_
                 hi = over_lanes<16>(hi, max_nan);
             }
             constexpr float TOP = (float)((1 << BITS) - 1);
-            const f16 m16 = (f16)lo, s16 = (f16)((hi - lo) / TOP);
-            const float m = (float)m16, s = (float)s16;
+            const f16 m16 = (f16)lo;
+            const float m = (float)m16;
+            // With a min that has become an infinity the group stands for
+            // nothing: its scale is NaN, so that attention spoils what sees
+            // it instead of leaving out a key of score -inf.
+            const f16 s16 = (f16)(__builtin_isinf(m) ? __builtin_nanf("") : (hi - lo) / TOP);
+            const float s = (float)s16;
             u32 w[BITS / 4];
 #pragma unroll
             for (int i = 0; i < BITS / 4; ++i) w[i] = 0;

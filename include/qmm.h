@@ -396,7 +396,8 @@ typedef struct qmm_kv_cache {
  *   q_out fp16 [tokens][q_heads][head_dim]
  *   k, v: into slot slots[token] of the cache.  Per group: min fp16(lowest),
  *     scale fp16((highest - lowest) / (2^bits - 1)), code
- *     round((x - min) / scale) within 0 .. 2^bits - 1 (0 where the scale is 0).
+ *     round((x - min) / scale) within 0 .. 2^bits - 1 (0 where the scale is 0 or
+ *     not finite).
  *   k_out, v_out fp16 [tokens][kv_heads][head_dim] or NULL: what prompt
  *     attention reads; with out_cached the values that the cache stands for
  *     (fp16(scale * code + min)), else the rows before quantization.
@@ -407,8 +408,11 @@ typedef struct qmm_kv_cache {
  *   inv_freq fp32 [rot_dim / 2]; rot_dim 0 (no rotation, positions and
  *     inv_freq may be NULL) to head_dim, a multiple of 16.
  * q_heads 0 (q and q_out may be NULL) to 4096; rows 16-byte aligned (pointers
- * and strides); tokens below 2^24.  A value that is not finite, or beyond
- * fp16, makes its group's scale or min so: the group reads back as NaN.     */
+ * and strides); tokens below 2^24.  A group with a value that is not finite, or
+ * whose lowest value is beyond fp16, or whose spread is (over 2^bits - 1),
+ * gets a scale that is not finite and reads back as NaN.  Where the highest
+ * value alone is beyond fp16 the group is held as it is: exact as a key, as a
+ * value (and in k_out and v_out) infinite where it leaves fp16.              */
 QMM_API qmm_status qmm_kv_append(const qmm_kv_cache *cache /* host */, const void *q,
                                  const void *k, const void *v, int in_fp16, int64_t q_stride,
                                  int64_t k_stride, int64_t v_stride, const float *q_norm,
@@ -427,8 +431,10 @@ QMM_API qmm_status qmm_kv_append(const qmm_kv_cache *cache /* host */, const voi
  *   kv_lens int32 [n_seqs] (device): cached rows of a sequence, the q_len new
  *     ones included; values outside [0, max_kv_len] are clamped.
  *   Token i of q_len sees rows t < kv_len - q_len + 1 + i; one that sees no
- *     row gets zeros.  Rows behind kv_len may hold anything.  A value that is
- *     not finite reaches the tokens that see it and no others.
+ *     row gets zeros.  Rows behind kv_len may hold anything.  A value of v,
+ *     fp16(scale * code + min), that is not finite, and a score that is NaN or
+ *     +inf, reaches the tokens that see it and no others; a score of -inf
+ *     leaves its row out.
  *   max_kv_len (host): at most table_stride * page_size and below 2^30.
  *   scale multiplies the scores (before the softmax).
  *   workspace: device scratch, 16-byte aligned, for partial sums.  Its first
@@ -458,7 +464,8 @@ QMM_API size_t qmm_attn_cache_workspace_bytes(const qmm_kv_cache *cache /* host 
  *     rows seq_offsets[i] .. seq_offsets[i + 1] - 1, and row r of it sees rows
  *     seq_offsets[i] .. r.  Rows that no sequence covers are left as they were.
  *     Whatever the offsets hold, nothing outside the given rows is touched.
- *   A value that is not finite reaches the rows that see it and no others.
+ *   A value of v that is not finite, and a score that is NaN or +inf, reaches
+ *     the rows that see it and no others; a score of -inf leaves its key out.
  * head_dim 64 or 128; q_heads a multiple of kv_heads; k and v strides below
  * 2^23 (else QMM_ERR_UNSUPPORTED).  Probabilities are
  * rounded to fp16 for the second product; sums are fp32.                    */
