@@ -286,15 +286,15 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
             for (int n = 0; n < D / 32; ++n) o[n] = o[n] * f;
         }
         const float base = mx == NEG_INF ? 0.f : mx * sc;
-        // Probabilities are cut to fp16, and their sum is of the cut values:
-        // what the cutting takes away on average it takes from both sides of
-        // the quotient.
+        // Probabilities are rounded to fp16 for the second product (to the
+        // nearest: two in one instruction, as cutting them is), and their
+        // sum is of the rounded values, so that weights still add up to one.
         u32 w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i], sc, -base));
             const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i + 1], sc, -base));
-            w[i] = __builtin_bit_cast(u32, __builtin_amdgcn_cvt_pkrtz(p0, p1));
+            w[i] = as_u32(f16x2{(f16)p0, (f16)p1});
             sum = __builtin_amdgcn_fdot2(as_h2(w[i]), f16x2{(f16)1.f, (f16)1.f}, sum, false);
         }
         // V^T operand: lane (h, l32) wants value 32 n + l32 of keys
