@@ -40,8 +40,6 @@
 namespace qmm {
 namespace {
 
-typedef f16 f16x4v __attribute__((ext_vector_type(4)));
-
 constexpr int WAVES = 4;
 constexpr int TILE = 32;  // cached rows per wave step
 constexpr int STEP = CACHE_STEP;  // and per step of a work-group
@@ -138,18 +136,18 @@ struct Place {
 // LDS read.  m0 holds the LDS address and needs one instruction between its
 // write and its use; there is no register for the load to write, and the
 // address registers are read when it is issued.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is a reserved register
 __device__ __forceinline__ void rows_to_lds(const char* base, u32 offset, u32 to) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(offset), "s"(base), "s"(to) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(offset), "s"(base), "s"(to) : "memory", "m0");
 }
 __device__ __forceinline__ void rows_to_lds(const char* from, u32 to) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(from), "s"(to) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(from), "s"(to) : "memory", "m0");
 }
 __device__ __forceinline__ void words_to_lds(const char* from, u32 to) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(from), "s"(to) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(from), "s"(to) : "memory", "m0");
 }
-__device__ __forceinline__ u32 lds_address(const void* p) {
-    return (u32)(size_t)(const __attribute__((address_space(3))) char*)p;
-}
+#pragma clang diagnostic pop
 
 // Where things lie in a stage.  K: chunk q of row r of a half at
 // [r][q ^ fold(r)], so that the same chunk of 16 rows falls on 16 different

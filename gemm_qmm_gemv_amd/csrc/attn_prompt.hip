@@ -98,15 +98,15 @@ __device__ __forceinline__ float halves_max(float v) {
 // holds the LDS address and needs one instruction between its write and its
 // use.  There is no register for the load to write, and the address registers
 // are read when it is issued.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is a reserved register
 __device__ __forceinline__ void load_to_lds(u32x4 rsrc, u32 offset, u32 to) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  :
                  : "v"(offset), "s"(rsrc), "s"(to)
-                 : "memory");
+                 : "memory", "m0");
 }
-__device__ __forceinline__ u32 lds_address(const void* p) {
-    return (u32)(size_t)(const __attribute__((address_space(3))) char*)p;
-}
+#pragma clang diagnostic pop
 // Buffer descriptor of everything from p on (offsets are clamped by the caller).
 __device__ __forceinline__ u32x4 open_rsrc(const void* p) {
     const uint64_t a = reinterpret_cast<uint64_t>(p);

@@ -1,6 +1,6 @@
 // layer_device.h -- sums, minima and maxima over the lanes of a wave without
 // LDS: the data-parallel primitives of a row of 16 lanes, and on gfx950 the
-// swaps of rows and halves.
+// swaps of rows and halves; addresses in LDS.
 #pragma once
 
 #include "qmm_device.h"
@@ -58,6 +58,11 @@ __device__ __forceinline__ float over_halves(float v, F f) {
     const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
     const u32 a = r[0], b = r[1];
     return f(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+
+// Where in LDS p points, as the direct loads take it.
+__device__ __forceinline__ u32 lds_address(const void* p) {
+    return (u32)(size_t)(const __attribute__((address_space(3))) char*)p;
 }
 
 __device__ __forceinline__ float add_f32(float a, float b) { return a + b; }
