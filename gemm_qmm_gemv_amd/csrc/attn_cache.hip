@@ -133,19 +133,21 @@ struct Place {
 // 16 (or 4) bytes per lane from memory to LDS at `to` + 16 (4) * lane, without
 // passing through registers.  Instructions of their own text: the compiler,
 // were it to know that they write LDS, would wait for all of them before any
-// LDS read.  m0 holds the LDS address and needs one instruction between its
-// write and its use; there is no register for the load to write, and the
-// address registers are read when it is issued.
+// LDS read.  m0 holds the LDS address.  Scalar registers that a vector
+// instruction wrote may be read by a memory instruction five wait states later,
+// which the compiler sees to for its own instructions only: s_mov and s_nop
+// make up five.  There is no register for the load to write, and the address
+// registers are read when it is issued.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // m0 is a reserved register
 __device__ __forceinline__ void rows_to_lds(const char* base, u32 offset, u32 to) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(offset), "s"(base), "s"(to) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(offset), "s"(base), "s"(to) : "memory", "m0");
 }
 __device__ __forceinline__ void rows_to_lds(const char* from, u32 to) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(from), "s"(to) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(from), "s"(to) : "memory", "m0");
 }
 __device__ __forceinline__ void words_to_lds(const char* from, u32 to) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(from), "s"(to) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tglobal_load_lds_dword %0, off" : : "v"(from), "s"(to) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 

@@ -95,13 +95,15 @@ __device__ __forceinline__ float halves_max(float v) {
 // i's land at `to` + 16 i.  An instruction of its own text, because the
 // compiler waits for all loads before any later LDS read if it knows that
 // this one writes LDS; here readers do, before the barrier they share.  m0
-// holds the LDS address and needs one instruction between its write and its
-// use.  There is no register for the load to write, and the address registers
-// are read when it is issued.
+// holds the LDS address.  Scalar registers that a vector instruction wrote may
+// be read by a memory instruction five wait states later, which the compiler
+// sees to for its own instructions only: s_mov and s_nop make up five (the
+// same times as with the one that m0 needs).  There is no register for the
+// load to write, and the address registers are read when it is issued.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // m0 is a reserved register
 __device__ __forceinline__ void load_to_lds(u32x4 rsrc, u32 offset, u32 to) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  :
                  : "v"(offset), "s"(rsrc), "s"(to)
                  : "memory", "m0");

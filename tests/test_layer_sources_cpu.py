@@ -38,3 +38,17 @@ def test_there_are_statements():
 def test_a_written_m0_is_named(place, lines, body):
     if any(re.match(r"s_\w+\s+m0\b", x) for x in lines):
         assert re.search(r':[^:]*"m0"[^:]*$', body), place
+
+
+@pytest.mark.parametrize("place,lines,body", ALL, ids=[p for p, _, _ in ALL])
+def test_memory_instructions_wait_for_scalar_operands(place, lines, body):
+    # Five wait states lie between a vector instruction's write of a scalar register and a memory instruction's read of it;
+    # within a statement its own instructions have to make them up (an instruction is one, s_nop n is n + 1).
+    if not re.search(r'"s"\s*\(', body):
+        return
+    states = 0
+    for x in lines:
+        if re.match(r"(buffer|global|flat)_", x):
+            assert states >= 5, place
+        nop = re.match(r"s_nop\s+(\d+)", x)
+        states += int(nop[1]) + 1 if nop else 1
