@@ -387,13 +387,21 @@ hipError_t launch(const PromptArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Work-groups of 128 rows where there are two and a half or more for every
-// compute unit, else of 64 with two waves for every 32 rows, which halves the
-// longest chain of steps.  One prompt of 1500, 2048 and 3000 tokens, 32 heads of
-// 64 (1.5, 2 and 3 work-groups of 128 rows per unit): 24.6, 34.6 and 64.6 us
-// with 64 rows, 30.4, 40.7 and 61.4 with 128; of 128: 36.7, 57.9 and 112 against
-// 41.9, 59.7 and 98; 16 heads of 128, 3000 tokens (1.5): 60 against 77.  Four
-// waves for 32 rows gain 10 % at 512 and 1024 tokens and lose 20 % at 128.
+// Work-groups of 128 rows where there are enough for every compute unit, else
+// of 64 with two waves for every 32 rows, which halves the longest chain of
+// steps.  A long sequence is such a chain: up to two and a half work-groups of
+// 128 rows per unit 64 rows are faster (1, 2 and 3 of them, one prompt of 1000,
+// 2048 and 3000 tokens, 32 heads of 64: 17.3, 34.2 and 64.6 us with 64 rows, 23.1,
+// 41.1 and 61.4 with 128; two of 1000, 32 heads of 128: 41.0 against 46.8).  Short
+// packed ones have no chain, and reading each key for 64 rows only costs more
+// than it saves from two per unit on with heads of 64 and one and a half with
+// 128 (2 per unit, 16 of 128 tokens: 11.7 us with 64 rows and 9.9 with 128 at
+// head size 64, 21.2 and 16.5 at 128; 33 of up to 100, 1.6 per unit: 12.4 and
+// 12.8, 22.8 and 19.2; 1 per unit, 16 of 64: 7.1 and 7.5, 10.9 and 12.0).  The
+// host knows the mean length alone: 4 of 512 are faster with 128 rows (19.4
+// against 17.0, 28.2 against 25.6) and count as short, one of 1000 among eight
+// of up to 125, 1.6 per unit, would be with 64 at head size 128 (32.1 against 39.7).
+// Four waves for 32 rows gain 10 % at 512 and 1024 tokens and lose 20 % at 128.
 //
 // Tiles of 32 keys let three work-groups share a compute unit at head size 128
 // (8192 tokens, 32 heads: 558 us against 594 with 64 keys and two); at 64
@@ -402,7 +410,9 @@ hipError_t launch(const PromptArgs& a, hipStream_t st) {
 template <int D>
 hipError_t launch_rows(const PromptArgs& a, hipStream_t st) {
     const int64_t blocks = (a.tokens + 127) / 128 * a.q_heads;
-    if (blocks * 2 < 5 * (int64_t)a.cus && a.tokens <= 65535 * 64) return launch<D, 2, 2, 64>(a, st);
+    const bool lengthy = a.tokens >= 800 * a.n_seqs;
+    const int halves = lengthy ? 5 : D == 64 ? 4 : 3;  // of a work-group per unit
+    if (blocks * 2 < halves * (int64_t)a.cus && a.tokens <= 65535 * 64) return launch<D, 2, 2, 64>(a, st);
     return launch<D, 4, 1, D == 128 ? 32 : 64>(a, st);
 }
 
