@@ -24,6 +24,8 @@
 //   keys; O^T = V^T P^T takes them as its right operand as they are, with V^T
 //   read in the same order of keys.  A query row's maximum and sum need one
 //   exchange with lane l ^ 32.
+#include <type_traits>
+
 #include "layer_device.h"
 #include "layer_kernels.h"
 
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
     constexpr int BUF = BN * D;
     __shared__ __align__(1024) f16 lds[4 * BUF];
     __shared__ int lds_bad[2][BN], lds_any[2];
-    __shared__ int lds_lo[RW], lds_hi[RW], lds_late[RW];
+    __shared__ int lds_lo[RW], lds_hi[RW], lds_late[RW], lds_large[RW];
     f16* const lds_k = lds;
     f16* const lds_v = lds + 2 * BUF;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -181,7 +183,22 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
     const int wlo = covered ? __builtin_amdgcn_readlane(start, from) : 0x7fffffff;
     const int wlate = covered ? __builtin_amdgcn_readlane(start, to) : 0;
     const int whi = covered ? wrow0 + to : -1;
+    // Whether scores may be so large that s sc - mx sc has to be formed from
+    // s - mx (see the step).  mx sc as a rounded number is off by up to 2^-24 of
+    // itself: a factor that all probabilities of a row share and the quotient
+    // drops, but past 2^26 one of more than 2^4, which with the lag's 2^8 nears
+    // what fp16 holds.  With fp16 keys, whose rows are at most 65504 D^1/2 long,
+    // a score is that large only if the query's row is longer than 1024 D^-1/2 / sc
+    // (710 at D 128 and scale 128^-1/2).
+    float square = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) square = __builtin_amdgcn_fdot2(as_h2(qw[j][i]), as_h2(qw[j][i]), square, false);
+    square = over_halves(square, add_f32);
+    const bool large = __any(!(square * (D * sc * sc) <= 1024.f * 1024.f));
     if (lane == 0) {
+        lds_large[rw] = large;
         lds_lo[rw] = wlo;
         lds_hi[rw] = whi;
         lds_late[rw] = wlate;
@@ -189,16 +206,18 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
     if (tid < 2 * BN) (&lds_bad[0][0])[tid] = 0;
     if (tid < 2) lds_any[tid] = 0;
     __syncthreads();
-    int blo = 0x7fffffff, bhi = -1, blate = 0;
+    int blo = 0x7fffffff, bhi = -1, blate = 0, apart = 0;
 #pragma unroll
     for (int w = 0; w < RW; ++w) {
         blo = lds_lo[w] < blo ? lds_lo[w] : blo;
         bhi = lds_hi[w] > bhi ? lds_hi[w] : bhi;
         blate = lds_late[w] > blate ? lds_late[w] : blate;
+        apart |= lds_large[w];
     }
     blo = uniform(blo);
     bhi = uniform(bhi);
     blate = uniform(blate);
+    apart = uniform(apart);
     if (bhi < 0) return;
 
     f32x16 o[D / 32];
@@ -249,7 +268,7 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
     const int q16 = lane & 15, v_row = 4 * h + (q16 >> 2);
     const int v_lane = v_row * D + 8 * ((2 * (lane >> 4 & 1) + (q16 >> 1 & 1)) ^ v_swizzle<D>(v_row)) + 4 * (q16 & 1);
     // One step of 32 keys, number u of tile j, which lies in buffer j & 1.
-    auto step = [&](int j, int u, bool cleaned) {
+    auto step = [&](int j, int u, bool cleaned, auto apart) {
         const int t = blo + j * BN + 32 * u;
         if (t > whi || t + 31 < wlo) return;
         const int b = j & 1;
@@ -287,15 +306,16 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
 #pragma unroll
             for (int n = 0; n < D / 32; ++n) o[n] = o[n] * f;
         }
-        const float base = mx == NEG_INF ? 0.f : mx * sc;
+        // One multiply-add per score, or with large ones the difference first.
+        const float base = mx == NEG_INF ? 0.f : apart ? mx : mx * sc;
+        auto power = [&](float x) { return __builtin_amdgcn_exp2f(apart ? (x - base) * sc : __builtin_fmaf(x, sc, -base)); };
         // Probabilities are rounded to fp16 for the second product (to the
         // nearest: two in one instruction, as cutting them is), and their
         // sum is of the rounded values, so that weights still add up to one.
         u32 w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i], sc, -base));
-            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i + 1], sc, -base));
+            const float p0 = power(s[2 * i]), p1 = power(s[2 * i + 1]);
             w[i] = as_u32(f16x2{(f16)p0, (f16)p1});
             sum = __builtin_amdgcn_fdot2(as_h2(w[i]), f16x2{(f16)1.f, (f16)1.f}, sum, false);
         }
@@ -321,17 +341,23 @@ __global__ void __launch_bounds__(64 * RW * KW, BN == 32 ? 3 : 2) attn_prompt_ke
     // once per tile: each has waited for its own loads, so the tile is whole,
     // and none reads the other buffer any more, so it can be filled.
     fetch(0, 0);
-    for (int j = 0; j < tiles; ++j) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        const bool cleaned = partial(j);
-        if (cleaned) clean(j, j & 1);
-        __syncthreads();
-        if (j + 1 < tiles) fetch(j + 1, (j + 1) & 1);
-        constexpr int U = BN / 32;
+    auto run = [&](auto apart) {
+        for (int j = 0; j < tiles; ++j) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            const bool cleaned = partial(j);
+            if (cleaned) clean(j, j & 1);
+            __syncthreads();
+            if (j + 1 < tiles) fetch(j + 1, (j + 1) & 1);
+            constexpr int U = BN / 32;
 #pragma unroll 1
-        for (int u = 0; u < U; ++u)
-            if (KW == 1 || u % KW == kw) step(j, u, cleaned);
-    }
+            for (int u = 0; u < U; ++u)
+                if (KW == 1 || u % KW == kw) step(j, u, cleaned, apart);
+        }
+    };
+    if (__builtin_expect(apart, 0))
+        run(std::true_type{});
+    else
+        run(std::false_type{});
     sum = over_halves(sum, add_f32);
     if constexpr (KW > 1) {
         // The waves that share rows hand their sums to the first of them.
