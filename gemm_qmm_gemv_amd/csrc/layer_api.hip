@@ -59,6 +59,14 @@ qmm_status check_heads(int q_heads, int kv_heads, bool q_required) {
     return QMM_OK;
 }
 
+// The kernels form scale * log2(e), over a cache of codes 2^24 times that, and
+// products with scores in fp32: far above any use, infinities would come out.
+qmm_status check_scale(float scale) {
+    CHECK(std::isfinite(scale), QMM_ERR_INVALID_ARGUMENT, "scale is not finite");
+    CHECK(std::fabs(scale) <= 18446744073709551616.f, QMM_ERR_UNSUPPORTED, "scale=%g is beyond 2^64", (double)scale);
+    return QMM_OK;
+}
+
 // The cache's shape; its arrays too if they are going to be used.
 qmm_status check_cache(const qmm_kv_cache* c, bool arrays) {
     CHECK(c, QMM_ERR_INVALID_ARGUMENT, "NULL cache");
@@ -296,7 +304,7 @@ qmm_status qmm_attn_cache(const qmm_kv_cache* cache, const void* q, const int32_
                           float scale, void* workspace, size_t workspace_bytes, void* stream) {
     qmm_status st = check_attn_cache(cache, n_seqs > 0, n_seqs, q_len, q_heads, max_kv_len);
     if (st != QMM_OK) return st;
-    CHECK(std::isfinite(scale), QMM_ERR_INVALID_ARGUMENT, "scale is not finite");
+    if ((st = check_scale(scale)) != QMM_OK) return st;
     CHECK(workspace_bytes == 0 || workspace, QMM_ERR_INVALID_ARGUMENT, "workspace_bytes without a workspace");
     CHECK(aligned(workspace, 16), QMM_ERR_MISALIGNED, "workspace not 16-byte aligned");
     CHECK(table_stride >= 0 && table_stride < (1LL << 40), QMM_ERR_INVALID_ARGUMENT, "table_stride=%lld out of range",
@@ -342,7 +350,7 @@ qmm_status qmm_attn_prompt(const void* q, const void* k, const void* v, const in
     if ((st = check_heads(q_heads, kv_heads, true)) != QMM_OK) return st;
     CHECK(q_heads % kv_heads == 0, QMM_ERR_INVALID_ARGUMENT, "q_heads=%d is not a multiple of kv_heads=%d", q_heads,
           kv_heads);
-    CHECK(std::isfinite(scale), QMM_ERR_INVALID_ARGUMENT, "scale is not finite");
+    if ((st = check_scale(scale)) != QMM_OK) return st;
     CHECK(tokens >= 0 && n_seqs >= 0 && n_seqs < 0x7ffffffe, QMM_ERR_INVALID_ARGUMENT, "tokens=%lld or n_seqs=%lld out of range",
           (long long)tokens, (long long)n_seqs);
     CHECK(tokens <= 65535 * 128 && (tokens + 127) / 128 * q_heads <= MAX_BLOCKS, QMM_ERR_UNSUPPORTED,

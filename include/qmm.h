@@ -436,7 +436,8 @@ QMM_API qmm_status qmm_kv_append(const qmm_kv_cache *cache /* host */, const voi
  *     +inf, reaches the tokens that see it and no others; a score of -inf
  *     leaves its row out.
  *   max_kv_len (host): at most table_stride * page_size and below 2^30.
- *   scale multiplies the scores (before the softmax).
+ *   scale multiplies the scores (before the softmax); its magnitude is at most
+ *     2^64, else QMM_ERR_UNSUPPORTED.
  *   workspace: device scratch, 16-byte aligned, for partial sums.  Its first
  *     QMM_ATTN_COUNTER_BYTES bytes hold arrival counters: they must be zero
  *     before its first use (allocate it zeroed once), and every call leaves
@@ -467,7 +468,7 @@ QMM_API size_t qmm_attn_cache_workspace_bytes(const qmm_kv_cache *cache /* host 
  *   A value of v that is not finite, and a score that is NaN or +inf, reaches
  *     the rows that see it and no others; a score of -inf leaves its key out.
  * head_dim 64 or 128; q_heads a multiple of kv_heads; k and v strides below
- * 2^23 (else QMM_ERR_UNSUPPORTED).  Probabilities are
+ * 2^23, scale's magnitude at most 2^64 (else QMM_ERR_UNSUPPORTED).  Probabilities are
  * rounded to fp16 for the second product; sums are fp32.                    */
 QMM_API qmm_status qmm_attn_prompt(const void *q, const void *k, const void *v,
                                    const int32_t *seq_offsets, void *out, int64_t tokens,
