@@ -14,7 +14,8 @@
 // them, in the same launch.
 //
 // 64 histories of 4000 to 16384 rows, 4 key heads of 128, 4 bits (348 MB) take
-// 78 us, 4.5 TB/s.  What is left above the rate of a copy (5.3) is 6 us before the
+// 77 us, 4.5 TB/s; of 2000 to 8192 rows in 8 bits (369 MB) 77, 4.8, in fp16 (693 MB)
+// 128, 5.4.  What is left above the rate of a copy (5.3) is 6 us before the
 // first rows arrive and the ends: of the work-groups on a compute unit the one
 // that was launched first is served first and done first.  The vector units
 // alone would need 64 us.  Short calls are a chain of waits: lengths, page
@@ -33,7 +34,8 @@
 // Values are rounded once to fp16 (the value the cache stands for).  The
 // probabilities of quantized caches go in as fp16 high and low parts: the
 // matrix cores idle most of the time, and with V's rounding in the result a
-// second one of the same size would show.
+// second one of the same size would show.  Over an fp16 cache, where V is exact,
+// they are rounded to fp16 once.
 #include "layer_device.h"
 #include "layer_kernels.h"
 
@@ -126,8 +128,8 @@ struct Place {
 
 // ---- Quantized rows.  Their pieces are small (4 to 8 bytes per lane and
 // cached row) and asked for one by one they keep the address units busier than
-// the memory: 24 loads per step took 57 us of a 106 us call with all rows in
-// the caches.  So a step's rows come into LDS as they lie, 1 KiB per load, and
+// the memory: 24 loads per step took 57 us of a call of 106 us, in an earlier
+// form, with all rows in the caches.  So a step's rows come into LDS as they lie, 1 KiB per load, and
 // are taken apart from there.
 
 // 16 (or 4) bytes per lane from memory to LDS at `to` + 16 (4) * lane, without
@@ -722,9 +724,9 @@ __global__ void __launch_bounds__(64 * WAVES, cache_resident(BITS, D)) attn_cach
     auto steps_of = [&](int len) { return (uint32_t)(len + STEP - 1) / STEP; };
     // A unit is counted as START steps more than it has: what beginning and
     // joining a run costs.  With 0, 1, 2 and 4 of them drafts over 8 bits
-    // (5 steps a share) took 28.7, 27.3, 26.3 and 26.4 us, 17 ragged sequences (2
-    // steps) 22.0, 20.0, 20.3 and 20.3, 64 long histories (25 steps) 96 to 103
-    // with any of them.
+    // (5 steps a share) take 24.9, 22.8, 22.2 and 22.5 us, 17 ragged sequences (2
+    // steps) 16.9, 15.7, 15.3 and 15.1, one of 1500 rows 8.8, 10.7, 8.8 and 8.8, 64
+    // long histories (25 steps) 77 to 78 with any of them.
     auto size_of = [&](int len) { return len == 0 ? 0u : steps_of(len) + START; };
 
     Segment sg;
@@ -775,7 +777,8 @@ __global__ void __launch_bounds__(64 * WAVES, cache_resident(BITS, D)) attn_cach
         before -= own;
         total = uniform((int)(total * per_seq));
         // No more shares than make LEAST steps each (one sequence of 1500 rows
-        // with 1, 2 and 4: 11.4, 10.8 and 13.9 us).  Neighbouring shares go
+        // with 1, 2 and 4: 9.2, 8.8 and 11.8 us; 17 ragged ones 15.3, 15.3 and
+        // 14.6; drafts and long ones the same).  Neighbouring shares go
         // to one die (work-groups go round the eight), so row tiles that read
         // the same cached rows share its L2.
         uint32_t shares = total / LEAST;

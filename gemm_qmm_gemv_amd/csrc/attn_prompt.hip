@@ -8,12 +8,15 @@
 // have about the same load.  Short steps on many waves keep all three busy
 // best: a wave holds 32 query rows of one head and takes 32 keys a step, and
 // three (head size 128) or four waves on each SIMD are at different places of
-// it.  8192 tokens, 32 query and 4 key heads of 128: 558 us, 985 TFLOP/s, 84 %
-// of what a large fp16 matrix product of the library reaches on the card (1178;
-// the clock drops to 1.9 GHz under either).  Tried and slower there: two waves
-// per SIMD with the next step's scores formed early (593 us), the same with
-// matrix and vector instructions interleaved by hand (631), 64 rows per wave
-// (829), K and V staged through registers (645).
+// it.  8192 tokens, 32 query and 4 key heads of 128: 557 to 568 us among others,
+// 583 to 604 alone under a kernel trace: 910 to 987 TFLOP/s, 79 to 84 % of what a
+// large fp16 matrix product of the library reaches on the card (1146 to 1178; the
+// clock drops to 1.9 GHz under either); of 64: 334 us, 822 TFLOP/s, vector units
+// 77 % busy, as a score costs as much there and its products half.  Tried and
+// slower at 128, where this took 558: two waves per SIMD with the next step's
+// scores formed early (593 us), the same with matrix and vector instructions
+// interleaved by hand (631), 64 rows per wave (829), K and V staged through
+// registers (645).
 //
 // Query rows are cut by their place in the packing and not by sequence: a tile
 // of rows may hold the end of one sequence and several short ones, which costs
@@ -431,8 +434,8 @@ hipError_t launch(const PromptArgs& a, hipStream_t st) {
 //
 // Tiles of 32 keys let three work-groups share a compute unit at head size 128
 // (8192 tokens, 32 heads: 558 us against 594 with 64 keys and two); at 64
-// four fit either way, and fewer meetings win (343 us against 350, 9 packed
-// prompts of up to 700 tokens 33.2 against 34.6).
+// four fit either way, and fewer meetings won (2 % there, 4 % on 9 packed prompts
+// of up to 700 tokens).
 template <int D>
 hipError_t launch_rows(const PromptArgs& a, hipStream_t st) {
     const int64_t blocks = (a.tokens + 127) / 128 * a.q_heads;

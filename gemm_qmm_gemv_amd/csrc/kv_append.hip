@@ -10,8 +10,9 @@
 //     m = fp16(min), s = fp16((max - min) / (2^b - 1))  (NaN where m is infinite),
 //     code = round((x - m) / s) clamped to [0, 2^b - 1]  (0 where s = 0 or not finite)
 //
-// Bound by memory, and into 4 bits by the vector units as well (90 % busy with
-// 4096 tokens of 48 heads of 64).  A lane holds 8 neighbours of a row, so D/8 lanes make a
+// Bound by memory into fp16 (8192 tokens of 40 heads of 128: 56.6 us, 4.7 TB/s), by
+// the vector units into codes (4096 tokens of 48 heads of 64: 15 to 16 us into 4
+// bits and into 8, 3.5 TB/s, units 87 and 85 % busy).  A lane holds 8 neighbours of a row, so D/8 lanes make a
 // row and sums, minima and maxima over a row or group are butterflies within
 // those lanes.  The angle is formed in 64 bits: at position 131071 a 32-bit
 // product is off by up to 0.004 rad.  Sines and cosines depend on the token
@@ -249,9 +250,9 @@ __global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a, int tile_
             for (int i = 0; i < BITS / 4; ++i) w[i] = 0;
             float held[8];
             // One division for the group; each quotient is put right by what
-            // it leaves of the dividend, as nearly as a division would (4096
-            // tokens of 48 heads of 64 19.3 -> 17.8 us; without putting right 17.6,
-            // but more codes next to a border would go the other way).
+            // it leaves of the dividend, as nearly as a division would (8 % of a
+            // call of 4096 tokens of 48 heads of 64; without putting right 1 %
+            // more, but more codes next to a border would go the other way).
             const float inv = s > 0.f ? 1.f / s : 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -283,9 +284,9 @@ hipError_t launch(const AppendArgs& a, hipStream_t st) {
     // Up to 16 tokens share their sines and cosines; with fewer tokens one
     // per work-group, and the heads are cut so that the device is filled: 16
     // work-groups for each unit.  With 2, 4, 8, 16 and 32 of them 8192 tokens of
-    // 32 + 2 x 4 heads of 128 into an fp16 cache took 86, 60, 61, 52 and 51 us, 8192
-    // of 16 + 2 x 8 heads of 128 into 4 bits 57, 44, 45, 40 and 41, 4096 of 32 + 2 x 8
-    // heads of 64 into 4 bits 21.3, 16.8, 17.0, 17.7 and 20.0.
+    // 32 + 2 x 4 heads of 128 into an fp16 cache take 94, 62, 67, 56 and 53 us, 8192
+    // of 16 + 2 x 8 heads of 128 into 4 bits 76, 52, 51, 46 and 48, 4096 of 32 + 2 x 8
+    // heads of 64 into 4 bits 19.2, 14.4, 14.5, 15.1 and 17.3.
     const int64_t want = 16 * (int64_t)a.cus;
     int tile_log2 = 4;
     while (tile_log2 > 0 && (a.tokens + (1 << tile_log2) - 1) >> tile_log2 < want) --tile_log2;

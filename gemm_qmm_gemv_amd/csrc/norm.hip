@@ -6,8 +6,9 @@
 // Bound by memory: every operand is read once and every result written once.
 // A work-group holds one row in registers (PER runs of four per thread), so
 // both sums of squares and the two products cost no second read.  8192 rows of
-// 4096 with all operands (537 MB) take 97 us, 5.5 TB/s, the rate of a copy of
-// that size; with 512 threads a row 98, with 1024 110.  Sums of squares
+// 4096 with all operands (537 MB) take 94 us, 5.7 TB/s, the rate of a copy of
+// that size (5.4); 512 threads a row took 1 % more, 1024 13 %.  4096 rows of 4095
+// (268 MB), element by element, take 72 us, 3.8 TB/s.  Sums of squares
 // are fp32: lanes add their own terms, then the lanes of each wave, then the
 // waves' sums in wave order (a fixed order, so results repeat bit for bit).
 #include "layer_device.h"
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(T) norm_kernel(NormArgs a) {
     // Up to 2048 elements, where a call is a chain of latencies, weights and
     // gate are asked for with the rest (1.5 us for one row of 1024).  Longer
     // rows take them where they are used: held from the start they cost three
-    // waves of eight (8192 rows of 4096 with all operands: 99 against 97 us).
+    // waves of eight (8192 rows of 4096 with all operands: 2 % more).
     constexpr bool EARLY = PER <= 2;
     __shared__ float lds[2][T / 64];
     const int64_t row = blockIdx.x;

@@ -445,7 +445,8 @@ QMM_API qmm_status qmm_kv_append(const qmm_kv_cache *cache /* host */, const voi
  *     stream, whatever their shapes.  With less than
  *     qmm_attn_cache_workspace_bytes() long sequences are split less, with
  *     none not at all.  Calls that overlap need a workspace each.
- * q_len 1 to 256.                                                           */
+ * q_len 1 to 256.  Roundings to fp16: the output's; over codes that of the
+ * values of v, over fp16 rows that of the probabilities.  Sums are fp32.     */
 #define QMM_ATTN_COUNTER_BYTES (64u * 1024u)
 
 QMM_API qmm_status qmm_attn_cache(const qmm_kv_cache *cache /* host */, const void *q,
