@@ -190,7 +190,8 @@ def _dense(name: str, t: torch.Tensor | None, dtype: torch.dtype, *shape: int) -
         return
     if t.dtype != dtype:
         raise ValueError("%s is %s, not %s" % (name, t.dtype, dtype))
-    if not t.is_contiguous() or t.shape[-1:] != shape[-1:] or t.numel() < math.prod(shape):
+    flat = t.dim() == 1 and len(shape) > 1  # rows behind each other
+    if not t.is_contiguous() or (t.shape[-1:] != shape[-1:] and not flat) or t.numel() < math.prod(shape):
         raise ValueError("%s of shape %s and strides %s is not dense or not %s"
                          % (name, tuple(t.shape), t.stride(), list(shape)))
 

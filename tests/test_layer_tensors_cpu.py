@@ -45,7 +45,7 @@ def test_gates_of_another_shape_are_refused(calls, gate):
 @pytest.mark.parametrize("kw", [
     dict(y=torch.zeros(3, 96)[:, 8:72]), dict(y=torch.zeros(3, 64, dtype=F16)), dict(y=None), dict(residual=None),
     dict(residual=torch.zeros(1, 3, 64)), dict(h=torch.zeros(8, 64)), dict(x=torch.zeros(3, 64, dtype=F16)), dict(pre=None),
-    dict(pre=torch.zeros(1, 64), post=torch.zeros(64)),
+    dict(pre=torch.zeros(1, 64), post=torch.zeros(64)), dict(residual=torch.zeros(192), h=torch.zeros(192), x=torch.zeros(200, dtype=F16)),
 ])
 def test_operands_of_the_norm(calls, kw):
     norm(**kw)
@@ -55,7 +55,7 @@ def test_operands_of_the_norm(calls, kw):
 @pytest.mark.parametrize("name,t", [
     ("y", torch.zeros(3, 64, dtype=torch.bfloat16)), ("y", torch.zeros(3, 64, dtype=torch.float64)),
     ("residual", torch.zeros(3, 64, dtype=F16)), ("residual", torch.zeros(3, 80)[:, :64]), ("residual", torch.zeros(2, 64)),
-    ("residual", torch.zeros(3, 65)), ("residual", torch.zeros(1, 64).expand(3, 64)), ("h", torch.zeros(3, 64, dtype=torch.float64)),
+    ("residual", torch.zeros(3, 65)), ("residual", torch.zeros(191)), ("h", torch.zeros(384)[::2]), ("residual", torch.zeros(1, 64).expand(3, 64)), ("h", torch.zeros(3, 64, dtype=torch.float64)),
     ("h", torch.zeros(3, 80)[:, :64]), ("h", torch.zeros(64, 3).t()), ("x", torch.zeros(3, 64)),
     ("x", torch.zeros(3, 80, dtype=F16)[:, :64]), ("x", torch.zeros(2, 64, dtype=F16)), ("pre", torch.zeros(64, dtype=F16)),
     ("pre", torch.zeros(63)), ("pre", torch.zeros(128)[::2]), ("post", torch.zeros(64, dtype=F16)), ("post", torch.zeros(1)),
