@@ -26,6 +26,8 @@ __all__ = [
     "QMM_NOALLOC_SCRATCH_BYTES", "QMM_ATTN_COUNTER_BYTES",
     "KvCache", "qmm_norm_residual", "qmm_kv_append", "qmm_attn_cache", "qmm_attn_cache_workspace_bytes",
     "qmm_attn_prompt",
+    "qmm_moe_route", "qmm_moe_route_workspace_bytes", "qmm_quantize_rows", "qmm_gemm_i8", "qmm_moe_gemm_i8",
+    "qmm_moe_swiglu_i8", "qmm_moe_gather",
     "qmm_get_plan", "qmm_status_string", "qmm_last_error", "qmm_abi_version",
     "QMM_OK", "QMM_ERR_INVALID_ARGUMENT", "QMM_ERR_UNSUPPORTED", "QMM_ERR_MISALIGNED",
     "QMM_ERR_DEVICE", "EXPORTED_SYMBOLS",
@@ -45,6 +47,8 @@ EXPORTED_SYMBOLS = (
     "qmm_moe_swiglu", "qmm_gemv_residual", "qmm_moe_combine", "qmm_gemm_grouped",
     "qmm_gemm_grouped_workspace_bytes", "qmm_gemm_noalloc", "qmm_set_override",
     "qmm_norm_residual", "qmm_kv_append", "qmm_attn_cache", "qmm_attn_cache_workspace_bytes", "qmm_attn_prompt",
+    "qmm_moe_route", "qmm_moe_route_workspace_bytes", "qmm_quantize_rows", "qmm_gemm_i8", "qmm_moe_gemm_i8",
+    "qmm_moe_swiglu_i8", "qmm_moe_gather",
     "qmm_call_words", "qmm_get_plan", "qmm_status_string", "qmm_last_error", "qmm_abi_version",
 )
 
@@ -181,12 +185,21 @@ def load():
     lib.qmm_attn_cache_workspace_bytes.argtypes = [pc, i64, ci, ci, i64]
     lib.qmm_attn_cache_workspace_bytes.restype = sz
     lib.qmm_attn_prompt.argtypes = [p, p, p, p, p, i64, i64, ci, ci, ci, i64, i64, i64, i64, cf, p]
+    lib.qmm_moe_route.argtypes = [p, ci, i64, p, ci, ci, ci, ci, ci, ci, cf, p, p, p, p, p, p, p, p, sz, i64, ci, p]
+    lib.qmm_moe_route_workspace_bytes.argtypes = [i64, ci, ci]
+    lib.qmm_moe_route_workspace_bytes.restype = sz
+    lib.qmm_quantize_rows.argtypes = [p, ci, i64, p, p, i64, i64, p]
+    lib.qmm_gemm_i8.argtypes = [p, p, p, p, p, ci, i64, i64, i64, p]
+    lib.qmm_moe_gemm_i8.argtypes = [p, p, p, p, p, i64, p, p, ci, i64, i64, i64, i64, p]
+    lib.qmm_moe_swiglu_i8.argtypes = [p, p, p, p, p, p, p, i64, p, p, ci, i64, i64, i64, i64, p]
+    lib.qmm_moe_gather.argtypes = [p, ci, p, p, p, p, i64, ci, i64, i64, p]
     lib.qmm_call_words.argtypes = [ci, ctypes.c_char_p]
     lib.qmm_get_plan.argtypes = [ci, i64, i64, i64, ci, ci, ci, sz, ctypes.POINTER(_Plan)]
     for f in ("qmm_gemv", "qmm_gemm", "qmm_moe_gemm", "qmm_unpack", "qmm_get_plan",
               "qmm_gemv_batch_prepare", "qmm_gemv_batched", "qmm_gemv_swiglu", "qmm_gemm_f16out", "qmm_moe_swiglu",
               "qmm_gemv_residual", "qmm_moe_combine", "qmm_gemm_grouped", "qmm_gemm_noalloc",
               "qmm_set_override", "qmm_norm_residual", "qmm_kv_append", "qmm_attn_cache", "qmm_attn_prompt",
+              "qmm_moe_route", "qmm_quantize_rows", "qmm_gemm_i8", "qmm_moe_gemm_i8", "qmm_moe_swiglu_i8", "qmm_moe_gather",
               "qmm_call_words"):
         getattr(lib, f).restype = ci
     lib.qmm_status_string.argtypes = [ci]
@@ -379,6 +392,12 @@ _NORM_WORDS = struct.Struct("=6qd6qdq").pack
 _APPEND_WORDS = struct.Struct("=10qd12q").pack
 _CACHE_WORDS = struct.Struct("=10qd3q").pack
 _PROMPT_WORDS = struct.Struct("=14qdq").pack
+_ROUTE_WORDS = struct.Struct("=10qd12q").pack
+_QUANTIZE_WORDS = struct.Struct("=8q").pack
+_GEMM_I8_WORDS = struct.Struct("=10q").pack
+_MOE_GEMM_I8_WORDS = struct.Struct("=14q").pack
+_MOE_SWIGLU_I8_WORDS = struct.Struct("=16q").pack
+_GATHER_WORDS = struct.Struct("=11q").pack
 
 
 def _word(v):
@@ -444,6 +463,68 @@ def qmm_attn_prompt(q, k, v, seq_offsets, out, tokens, n_seqs, q_heads, kv_heads
                                                     v_stride, out_stride, scale, _stream(stream)))
     if status != QMM_OK:
         _check(status, "qmm_attn_prompt")
+
+
+def qmm_moe_route(logits, logits_fp16, logits_stride, bias, sigmoid, n_groups, top_groups, group_best, top_k, renormalize,
+                  scale, keep, expert_ids, weights, pair_row, expert_offsets, pair_token, pair_weight, workspace,
+                  workspace_bytes, tokens, n_experts, stream=None) -> None:
+    """Scores to experts and weights, and the rows grouped by expert; asynchronous."""
+    status = load().qmm_call_words(4, _ROUTE_WORDS(_word(logits), logits_fp16, logits_stride, _word(bias), sigmoid, n_groups,
+                                                   top_groups, group_best, top_k, renormalize, scale, _word(keep),
+                                                   _word(expert_ids), _word(weights), _word(pair_row),
+                                                   _word(expert_offsets), _word(pair_token), _word(pair_weight),
+                                                   _word(workspace), workspace_bytes, tokens, n_experts, _stream(stream)))
+    if status != QMM_OK:
+        _check(status, "qmm_moe_route")
+
+
+def qmm_moe_route_workspace_bytes(tokens, n_experts, top_k) -> int:
+    return int(load().qmm_moe_route_workspace_bytes(int(tokens), int(n_experts), int(top_k)))
+
+
+def qmm_quantize_rows(x, x_fp16, x_stride, codes, scales, rows, k, stream=None) -> None:
+    """codes = round(x / scale), scale = max |x| / 127 of each row; asynchronous."""
+    status = load().qmm_call_words(5, _QUANTIZE_WORDS(_word(x), x_fp16, x_stride, _word(codes), _word(scales), rows, k,
+                                                      _stream(stream)))
+    if status != QMM_OK:
+        _check(status, "qmm_quantize_rows")
+
+
+def qmm_gemm_i8(w, w_scales, x, x_scales, y, y_fp16, m, n, k, stream=None) -> None:
+    """y[m][n] = x_scales[m] w_scales[n] sum_k x[m][k] w[n][k] in 8-bit integers; asynchronous."""
+    status = load().qmm_call_words(6, _GEMM_I8_WORDS(_word(w), _word(w_scales), _word(x), _word(x_scales), _word(y), y_fp16,
+                                                     m, n, k, _stream(stream)))
+    if status != QMM_OK:
+        _check(status, "qmm_gemm_i8")
+
+
+def qmm_moe_gemm_i8(w, w_scales, x, x_scales, x_rows, x_rows_count, expert_offsets, y, y_fp16, p_rows, n_experts, n, k,
+                    stream=None) -> None:
+    """The 8-bit product over rows grouped by expert; asynchronous."""
+    status = load().qmm_call_words(7, _MOE_GEMM_I8_WORDS(_word(w), _word(w_scales), _word(x), _word(x_scales), _word(x_rows),
+                                                         x_rows_count, _word(expert_offsets), _word(y), y_fp16, p_rows,
+                                                         n_experts, n, k, _stream(stream)))
+    if status != QMM_OK:
+        _check(status, "qmm_moe_gemm_i8")
+
+
+def qmm_moe_swiglu_i8(gate_w, gate_scales, up_w, up_scales, x, x_scales, x_rows, x_rows_count, expert_offsets, h, h_fp16,
+                      p_rows, n_experts, n, k, stream=None) -> None:
+    """h[p] = silu(gate[p]) * up[p] in 8-bit integers over rows grouped by expert; asynchronous."""
+    status = load().qmm_call_words(8, _MOE_SWIGLU_I8_WORDS(_word(gate_w), _word(gate_scales), _word(up_w), _word(up_scales),
+                                                           _word(x), _word(x_scales), _word(x_rows), x_rows_count,
+                                                           _word(expert_offsets), _word(h), h_fp16, p_rows, n_experts, n,
+                                                           k, _stream(stream)))
+    if status != QMM_OK:
+        _check(status, "qmm_moe_swiglu_i8")
+
+
+def qmm_moe_gather(rows, rows_fp16, pair_row, weights, residual, y, tokens, top_k, p_rows, n, stream=None) -> None:
+    """y[t] = residual[t] + sum_j weights[t][j] rows[pair_row[t][j]] in a fixed order; asynchronous."""
+    status = load().qmm_call_words(9, _GATHER_WORDS(_word(rows), rows_fp16, _word(pair_row), _word(weights), _word(residual),
+                                                    _word(y), tokens, top_k, p_rows, n, _stream(stream)))
+    if status != QMM_OK:
+        _check(status, "qmm_moe_gather")
 
 
 def qmm_unpack(w_packed, codes, n, k, bits, stream=None) -> None:

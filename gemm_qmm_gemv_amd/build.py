@@ -17,7 +17,9 @@ LIB = os.path.join(HERE, "libqmm.so")
 SOURCES = [("qmm_api.hip", [], "qmm_api.o"), ("gemm.hip", [], "gemm.o"), ("gemm_wl.hip", [], "gemm_wl.o"),
            ("unpack.hip", [], "unpack.o"), ("layer_api.hip", [], "layer_api.o"), ("norm.hip", [], "norm.o"),
            ("kv_append.hip", [], "kv_append.o"), ("attn_cache.hip", [], "attn_cache.o"),
-           ("attn_prompt.hip", [], "attn_prompt.o")] + [
+           ("attn_prompt.hip", [], "attn_prompt.o"), ("moe_api.hip", [], "moe_api.o"),
+           ("moe_route.hip", [], "moe_route.o"), ("quantize.hip", [], "quantize.o"),
+           ("gemm_i8.hip", [], "gemm_i8.o"), ("moe_gather.hip", [], "moe_gather.o")] + [
     ("gemv_bits.hip", ["-DQMM_BITS=%d" % b], "gemv_b%d.o" % b) for b in (2, 3, 4, 5, 6, 8, 16)]
 ARCH = os.environ.get("QMM_OFFLOAD_ARCH", "gfx950")
 

@@ -96,24 +96,6 @@ __device__ __forceinline__ float halves_max(float v) {
     return over_halves(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// 16 bytes per lane from memory to LDS without passing through registers: lane
-// i's land at `to` + 16 i.  An instruction of its own text, because the
-// compiler waits for all loads before any later LDS read if it knows that
-// this one writes LDS; here readers do, before the barrier they share.  m0
-// holds the LDS address.  Scalar registers that a vector instruction wrote may
-// be read by a memory instruction five wait states later, which the compiler
-// sees to for its own instructions only: s_mov and s_nop make up five (the
-// same times as with the one that m0 needs).  There is no register for the
-// load to write, and the address registers are read when it is issued.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"  // m0 is a reserved register
-__device__ __forceinline__ void load_to_lds(u32x4 rsrc, u32 offset, u32 to) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                 :
-                 : "v"(offset), "s"(rsrc), "s"(to)
-                 : "memory", "m0");
-}
-#pragma clang diagnostic pop
 // Buffer descriptor of everything from p on (offsets are clamped by the caller).
 __device__ __forceinline__ u32x4 open_rsrc(const void* p) {
     const uint64_t a = reinterpret_cast<uint64_t>(p);

@@ -4,11 +4,11 @@
 // no allocation, no synchronization, no state between calls.
 #include <hip/hip_runtime.h>
 
-#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstring>
 
+#include "api_checks.h"
 #include "layer_kernels.h"
 
 using namespace qmm;
@@ -16,35 +16,6 @@ using namespace qmm;
 namespace {
 
 constexpr int64_t MAX_BLOCKS = (1LL << 24) - 1;  // of 256 threads: HIP counts a launch's threads in 32 bits
-
-#define CHECK(cond, status, ...)                        \
-    do {                                                \
-        if (!(cond)) return report(status, __VA_ARGS__); \
-    } while (0)
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Compute units of the current device, asked for once per device.
-std::atomic<int> g_cus[64];
-
-qmm_status current_cus(int* cus) {
-    int dev = 0;
-    if (hipGetDevice(&dev) == hipSuccess) {
-        std::atomic<int>* known = dev >= 0 && dev < 64 ? &g_cus[dev] : nullptr;
-        if (known && (*cus = known->load(std::memory_order_relaxed)) > 0) return QMM_OK;
-        if (hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && *cus > 0) {
-            if (known) known->store(*cus, std::memory_order_relaxed);
-            return QMM_OK;
-        }
-    }
-    (void)hipGetLastError();
-    return report(QMM_ERR_DEVICE, "no HIP device available");
-}
-
-qmm_status launched(hipError_t e, const char* what) {
-    if (e != hipSuccess) return report(QMM_ERR_DEVICE, "%s launch failed: %s", what, hipGetErrorString(e));
-    return report(QMM_OK, "");
-}
 
 qmm_status check_head_dim(int d) {
     CHECK(d > 0, QMM_ERR_INVALID_ARGUMENT, "head_dim=%d must be positive", d);
@@ -393,6 +364,32 @@ qmm_status qmm_call_words(int call, const void* words) {
             std::memcpy(a.w, words, 16 * 8);
             return qmm_attn_prompt(a.p(0), a.p(1), a.p(2), a.p<int32_t>(3), a.p(4), a.w[5], a.w[6], a.i(7), a.i(8), a.i(9),
                                    a.w[10], a.w[11], a.w[12], a.w[13], a.f(14), a.p(15));
+        case QMM_CALL_MOE_ROUTE:
+            std::memcpy(a.w, words, 23 * 8);
+            return qmm_moe_route(a.p(0), a.i(1), a.w[2], a.p<float>(3), a.i(4), a.i(5), a.i(6), a.i(7), a.i(8), a.i(9),
+                                 a.f(10), a.p<uint8_t>(11), a.p<int32_t>(12), a.p<float>(13), a.p<int32_t>(14),
+                                 a.p<int32_t>(15), a.p<int32_t>(16), a.p<float>(17), a.p(18), (size_t)a.w[19], a.w[20],
+                                 a.i(21), a.p(22));
+        case QMM_CALL_QUANTIZE_ROWS:
+            std::memcpy(a.w, words, 8 * 8);
+            return qmm_quantize_rows(a.p(0), a.i(1), a.w[2], a.p<int8_t>(3), a.p<float>(4), a.w[5], a.w[6], a.p(7));
+        case QMM_CALL_GEMM_I8:
+            std::memcpy(a.w, words, 10 * 8);
+            return qmm_gemm_i8(a.p<int8_t>(0), a.p<float>(1), a.p<int8_t>(2), a.p<float>(3), a.p(4), a.i(5), a.w[6], a.w[7],
+                               a.w[8], a.p(9));
+        case QMM_CALL_MOE_GEMM_I8:
+            std::memcpy(a.w, words, 14 * 8);
+            return qmm_moe_gemm_i8(a.p<int8_t>(0), a.p<float>(1), a.p<int8_t>(2), a.p<float>(3), a.p<int32_t>(4), a.w[5],
+                                   a.p<int32_t>(6), a.p(7), a.i(8), a.w[9], a.w[10], a.w[11], a.w[12], a.p(13));
+        case QMM_CALL_MOE_SWIGLU_I8:
+            std::memcpy(a.w, words, 16 * 8);
+            return qmm_moe_swiglu_i8(a.p<int8_t>(0), a.p<float>(1), a.p<int8_t>(2), a.p<float>(3), a.p<int8_t>(4),
+                                     a.p<float>(5), a.p<int32_t>(6), a.w[7], a.p<int32_t>(8), a.p(9), a.i(10), a.w[11],
+                                     a.w[12], a.w[13], a.w[14], a.p(15));
+        case QMM_CALL_MOE_GATHER:
+            std::memcpy(a.w, words, 11 * 8);
+            return qmm_moe_gather(a.p(0), a.i(1), a.p<int32_t>(2), a.p<float>(3), a.p<float>(4), a.p<float>(5), a.w[6], a.i(7),
+                                  a.w[8], a.w[9], a.p(10));
     }
     return report(QMM_ERR_INVALID_ARGUMENT, "call=%d is none of QMM_CALL_*", call);
 }

@@ -1,6 +1,7 @@
 // layer_device.h -- sums, minima and maxima over the lanes of a wave without
 // LDS: the data-parallel primitives of a row of 16 lanes, and on gfx950 the
-// swaps of rows and halves; addresses in LDS.
+// swaps of rows and halves; addresses in LDS and
+// loads that go there directly.
 #pragma once
 
 #include "qmm_device.h"
@@ -64,6 +65,25 @@ __device__ __forceinline__ float over_halves(float v, F f) {
 __device__ __forceinline__ u32 lds_address(const void* p) {
     return (u32)(size_t)(const __attribute__((address_space(3))) char*)p;
 }
+
+// 16 bytes per lane from memory to LDS without passing through registers: lane
+// i's land at `to` + 16 i.  An instruction of its own text, because the
+// compiler waits for all loads before any later LDS read if it knows that
+// this one writes LDS; here readers do, before the barrier they share.  m0
+// holds the LDS address.  Scalar registers that a vector instruction wrote may
+// be read by a memory instruction five wait states later, which the compiler
+// sees to for its own instructions only: s_mov and s_nop make up five (the
+// same times as with the one that m0 needs).  There is no register for the
+// load to write, and the address registers are read when it is issued.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is a reserved register
+__device__ __forceinline__ void load_to_lds(u32x4 rsrc, u32 offset, u32 to) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :
+                 : "v"(offset), "s"(rsrc), "s"(to)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
 
 __device__ __forceinline__ float add_f32(float a, float b) { return a + b; }
 

@@ -477,11 +477,125 @@ QMM_API qmm_status qmm_attn_prompt(const void *q, const void *k, const void *v,
                                    int64_t q_stride, int64_t k_stride, int64_t v_stride,
                                    int64_t out_stride, float scale, void *stream);
 
-/* One of the four calls above with its arguments as 64-bit words in their order
- * (pointers and whole numbers as int64, float as double): for bindings in
- * which every argument of a foreign call costs time.  Same checks, same errors.
- * Words per call: 15, 23, 14 and 16.                                        */
-enum { QMM_CALL_NORM_RESIDUAL = 0, QMM_CALL_KV_APPEND = 1, QMM_CALL_ATTN_CACHE = 2, QMM_CALL_ATTN_PROMPT = 3 };
+/* ---- A mixture of experts' feed-forward block ---------------------------
+ * What stands around the experts' products: qmm_moe_route turns the router's
+ * scores into experts, weights and the rows grouped by expert that
+ * qmm_moe_gemm, qmm_moe_swiglu and the 8-bit products below take (its
+ * pair_token is their x_rows), and qmm_moe_gather adds the experts' rows up by
+ * token.  The rules at the top of this file hold; results repeat bit for bit.
+ *
+ * Routing, per token of n_experts scores l (fp32, or fp16 with logits_fp16; rows
+ * logits_stride elements apart):
+ *   s = softmax(l), or sigmoid(l) if `sigmoid`;  c = s + bias (bias fp32
+ *     [n_experts], or NULL: c = s)
+ *   n_groups > 1: expert e is of group e / (n_experts / n_groups); a group's
+ *     score is the sum of its group_best (1 or 2) highest c, and only experts of
+ *     the top_groups groups of highest score can be chosen
+ *   the top_k experts of highest c, in falling order of c
+ *   w = s[chosen], divided by their sum if `renormalize`, times scale
+ * Of equals the lower group and the lower expert come first.  Without a bias
+ * the c are in the order of the logits, exactly; sums of them, and c with a
+ * bias, are formed in 64 bits.
+ *   A logit of -inf scores 0 (it is chosen only where nothing else is left); a
+ *     token of nothing else gets weights of 0.  A NaN logit is placed as -inf and
+ *     makes the token's weights NaN, and so does +inf under softmax (where the
+ *     others' scores are then 0).  A c that is NaN is placed as -inf.
+ *   keep uint8 [tokens] or NULL: a token of 0 (padding) gets experts -1, weights 0
+ *     and no row.
+ *   expert_ids int32, weights fp32 [tokens][top_k]
+ *   expert_offsets int32 [n_experts + 1], or NULL: nothing is grouped, and what
+ *     follows is not looked at.  The pairs (token, choice) are sorted by expert,
+ *     within an expert by token; expert e's rows are expert_offsets[e] ..
+ *     expert_offsets[e + 1] - 1.
+ *   pair_row int32 [tokens][top_k] or NULL: row of each pair (-1: none)
+ *   pair_token int32, pair_weight fp32 [tokens * top_k], or NULL: token and
+ *     weight of each row; behind the last row they are left as they were.
+ *   workspace: device scratch of qmm_moe_route_workspace_bytes(), 16-byte aligned,
+ *     needed only to group (else QMM_ERR_INVALID_ARGUMENT); it may hold anything.
+ *     Calls that overlap need a workspace each.
+ * n_experts at most 1024, n_groups and top_k at most 64, tokens below 2^24, else
+ * QMM_ERR_UNSUPPORTED.  tokens 0: the offsets are set to 0.  No output may
+ * overlap an input or another output.                                       */
+QMM_API qmm_status qmm_moe_route(const void *logits, int logits_fp16, int64_t logits_stride,
+                                 const float *bias, int sigmoid, int n_groups, int top_groups,
+                                 int group_best, int top_k, int renormalize, float scale,
+                                 const uint8_t *keep, int32_t *expert_ids, float *weights,
+                                 int32_t *pair_row, int32_t *expert_offsets, int32_t *pair_token,
+                                 float *pair_weight, void *workspace, size_t workspace_bytes,
+                                 int64_t tokens, int n_experts, void *stream);
+QMM_API size_t qmm_moe_route_workspace_bytes(int64_t tokens, int n_experts, int top_k);
+
+/* The experts' rows back to their tokens, in a fixed order (qmm_moe_combine adds
+ * in no fixed order, inside the last product):
+ *   y[t] = residual[t] + sum_j weights[t][j] * rows[pair_row[t][j]]
+ *   rows fp32 (fp16 with rows_fp16) [p_rows][n]; pair_row int32, weights fp32
+ *   [tokens][top_k], as qmm_moe_route gives them; a row outside [0, p_rows) adds
+ *   nothing.  residual fp32 [tokens][n] or NULL (zero); it may be y.
+ *   y fp32 [tokens][n] (written).
+ * Sums are fp32, in the order of j, the residual last.  top_k at most 64, tokens below 2^24,
+ * n below 2^22, else QMM_ERR_UNSUPPORTED.  Pointers aligned to their elements;
+ * 16-byte aligned rows (n a multiple of 8) are faster.                      */
+QMM_API qmm_status qmm_moe_gather(const void *rows, int rows_fp16, const int32_t *pair_row,
+                                  const float *weights, const float *residual, float *y,
+                                  int64_t tokens, int top_k, int64_t p_rows, int64_t n,
+                                  void *stream);
+
+/* Products in 8-bit integers, with a scale for each row of either side
+ * (prefill at twice the matrix cores' rate for fp16, and half of its bytes).
+ *
+ * Activations to codes, per row of k values: scale = max |x| / 127 (fp32), code
+ * = round(x / scale), ties to even, within -127 .. 127 (0 where the scale is 0);
+ * the row's values are scale * code.
+ *   x fp32, or fp16 with x_fp16; rows x_stride elements apart
+ *   codes int8 [rows][k], 16-byte aligned; scales fp32 [rows]
+ * A row with a value that is not finite gets the scale NaN and codes 0, so
+ * whatever it is multiplied with is NaN.  k a multiple of 32, at most 32768,
+ * rows below 2^22 (else QMM_ERR_UNSUPPORTED).                               */
+QMM_API qmm_status qmm_quantize_rows(const void *x, int x_fp16, int64_t x_stride, int8_t *codes,
+                                     float *scales, int64_t rows, int64_t k, void *stream);
+
+/* y[i][j] = x_scales[i] * w_scales[j] * sum_k x[i][k] * w[j][k]
+ *   w int8 [n][k] with w_scales fp32 [n]; x int8 [m][k] with x_scales fp32 [m];
+ *   any codes from -128 to 127.  y fp32 [m][n], or fp16 with y_fp16.
+ * The sums are exact; scaling is fp32, and fp16 outputs are rounded once more.
+ * w, x and y 16-byte aligned, scales 4-byte; k a multiple of 32, at most 32768;
+ * one matrix and the activation block each below 4 GiB (else
+ * QMM_ERR_UNSUPPORTED).  Any m and n; y must not overlap an input.          */
+QMM_API qmm_status qmm_gemm_i8(const int8_t *w, const float *w_scales, const int8_t *x,
+                               const float *x_scales, void *y, int y_fp16, int64_t m, int64_t n,
+                               int64_t k, void *stream);
+
+/* The same over rows grouped by expert, with stacks w int8 [n_experts][n][k] and
+ * w_scales fp32 [n_experts][n]: row p of expert e's range reads activation row
+ * x_rows[p] (int32 [p_rows]; p if NULL) of x_rows_count.  expert_offsets, rows
+ * with an activation index out of range (NaN) and rows that no expert covers
+ * (left as they were) are as for qmm_moe_gemm; expert_offsets NULL with one
+ * expert: all rows are its.                                                 */
+QMM_API qmm_status qmm_moe_gemm_i8(const int8_t *w, const float *w_scales, const int8_t *x,
+                                   const float *x_scales, const int32_t *x_rows,
+                                   int64_t x_rows_count, const int32_t *expert_offsets, void *y,
+                                   int y_fp16, int64_t p_rows, int64_t n_experts, int64_t n,
+                                   int64_t k, void *stream);
+
+/* Gate and up products of the selected experts in one launch:
+ *   h[p][j] = silu(g[p][j]) * u[p][j], g and u as qmm_moe_gemm_i8 over the two
+ *   stacks, silu(v) = v / (1 + e^-v).  h fp32, or fp16 with h_fp16.          */
+QMM_API qmm_status qmm_moe_swiglu_i8(const int8_t *gate_w, const float *gate_scales,
+                                     const int8_t *up_w, const float *up_scales, const int8_t *x,
+                                     const float *x_scales, const int32_t *x_rows,
+                                     int64_t x_rows_count, const int32_t *expert_offsets, void *h,
+                                     int h_fp16, int64_t p_rows, int64_t n_experts, int64_t n,
+                                     int64_t k, void *stream);
+
+/* One of the calls above, from qmm_norm_residual on, with its arguments as 64-bit
+ * words in their order (pointers and whole numbers as int64, float as double):
+ * for bindings in which every argument of a foreign call costs time.  Same
+ * checks, same errors.  Words per call: 15, 23, 14, 16, 23, 8, 10, 14, 16 and 11. */
+enum {
+    QMM_CALL_NORM_RESIDUAL = 0, QMM_CALL_KV_APPEND = 1, QMM_CALL_ATTN_CACHE = 2, QMM_CALL_ATTN_PROMPT = 3,
+    QMM_CALL_MOE_ROUTE = 4, QMM_CALL_QUANTIZE_ROWS = 5, QMM_CALL_GEMM_I8 = 6, QMM_CALL_MOE_GEMM_I8 = 7,
+    QMM_CALL_MOE_SWIGLU_I8 = 8, QMM_CALL_MOE_GATHER = 9
+};
 
 QMM_API qmm_status qmm_call_words(int call, const void *words);
 
