@@ -6,7 +6,8 @@
 //
 // Sums of products are exact in 32-bit integers, whatever their order, so K
 // can be cut anywhere and results repeat bit for bit.
-#include <type_traits>
+#include <algorithm>
+#include <cmath>
 
 #include "layer_device.h"
 #include "moe_kernels.h"
@@ -137,31 +138,36 @@ __global__ void __launch_bounds__(64 * W) rows_i8_kernel(GemmI8Args a) {
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int c = 0; c < MB; ++c) acc[s][b][c] = i32x4{0, 0, 0, 0};
-    // 64 codes a step; behind K the loads give zeros.
-    const int steps = (a.k + 63) / 64;
-#pragma unroll 2
-    for (int st = wave; st < steps; st += W) {
-        const int k = st * 64 + 16 * piece;
-        const bool in = k < a.k;
-        i32x4 w[S][NB], x[MB];
+    // 128 codes of each row at a time, in two steps of the matrix instruction;
+    // behind K the loads give zeros.
+    const int chunks = (a.k + 127) / 128;
+    for (int ch = wave; ch < chunks; ch += W) {
+        i32x4 w[2][S][NB], x[2][MB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const u32 at = in && woff[b] < wbytes ? woff[b] + (u32)k : wbytes;
-            w[0][b] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, at, 0, 0));
-            if constexpr (GLU) w[S - 1][b] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(ur, at, 0, 0));
+        for (int q = 0; q < 2; ++q) {
+            const int k = ch * 128 + 64 * q + 16 * piece;
+            const bool in = k < a.k;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const u32 at = in && woff[b] < wbytes ? woff[b] + (u32)k : wbytes;
+                w[q][0][b] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, at, 0, 0));
+                if constexpr (GLU) w[q][S - 1][b] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(ur, at, 0, 0));
+            }
+#pragma unroll
+            for (int c = 0; c < MB; ++c) {
+                const u32 at = in && xoff[c] < xbytes ? xoff[c] + (u32)k : xbytes;
+                x[q][c] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, at, 0, 0));
+            }
         }
 #pragma unroll
-        for (int c = 0; c < MB; ++c) {
-            const u32 at = in && xoff[c] < xbytes ? xoff[c] + (u32)k : xbytes;
-            x[c] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, at, 0, 0));
-        }
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+            for (int s = 0; s < S; ++s)
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int c = 0; c < MB; ++c)
-                    acc[s][b][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s][b], x[c], acc[s][b][c], 0, 0, 0);
+                    for (int c = 0; c < MB; ++c)
+                        acc[s][b][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[q][s][b], x[q][c], acc[s][b][c], 0, 0, 0);
     }
 #pragma unroll
     for (int s = 0; s < S; ++s)
@@ -199,122 +205,382 @@ __global__ void __launch_bounds__(64 * W) rows_i8_kernel(GemmI8Args a) {
 // gated); both sides go straight from memory to LDS, 128 codes a step, two
 // stages.  LDS rows are 128 bytes of eight 16-byte pieces; piece q of row r is
 // in slot q ^ f(r), so that sixteen rows' same piece lies on all banks.
+//
+// A work-group stays for several tiles: the first stage of the next one is
+// fetched during the last step of this one, and its sums leave through the
+// stage that this step has read, while the other fills.
+constexpr int BK = 128;
 __device__ __forceinline__ int slot_of(int r, int q) { return q ^ ((r & 7) ^ ((r >> 3) & 1)); }
 
-template <int WM, int WN, int MF, int NF, bool GLU>
-__global__ void __launch_bounds__(64 * WM * WN) tile_i8_kernel(GemmI8Args a) {
-    constexpr int S = GLU ? 2 : 1, WAVES = WM * WN;
-    constexpr int BM = 32 * MF * WM, BN = 32 * NF * WN;  // columns of each stack
-    constexpr int BK = 128, ROWS = BM + S * BN, STAGE = ROWS * BK;
-    constexpr int LOADS = ROWS / 8 / WAVES;  // of one kilobyte, eight rows, per wave
-    static_assert(ROWS % (8 * WAVES) == 0, "whole loads");
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
-    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
-    const int ncols = (int)((a.n + BN - 1) / BN);
-    const RowTile rt = find_rows(a, (int)(blockIdx.x / ncols), BM);
-    if (rt.from >= rt.to) return;
-    const int64_t n0 = (int64_t)(blockIdx.x % ncols) * BN;
-    const u32 wbytes = (u32)(a.n * a.k), xbytes = (u32)(a.x_rows_count * a.k);
-    const int64_t stack = (int64_t)rt.e * a.n * a.k;
-    const u32x4 wr = bounded_rsrc(a.w + stack, wbytes), xr = bounded_rsrc(a.x, xbytes);
-    const u32x4 ur = GLU ? bounded_rsrc(a.w2 + stack, wbytes) : wr;
-    // Load i of this wave brings LDS rows 8 (LOADS wave + i) .. + 7: first the
-    // activations', then the gate's (or the only) columns', then the up's.
-    u32 off[LOADS];
-    int at_k[LOADS];
+// Work-group barrier behind this wave's LDS reads and writes, and its loads.
+__device__ __forceinline__ void loads_barrier() {
+    __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0), lgkmcnt(0)
+    asm volatile("s_barrier" ::: "memory");
+}
+// The same without the loads.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_s_waitcnt(15 | 3 << 14 | 7 << 4);  // lgkmcnt(0)
+    asm volatile("s_barrier" ::: "memory");
+}
+
+// Where each expert's row tiles begin: table [2][experts + 1], filled by the
+// first wave: tiles before (behind the last expert: all), offsets inside the
+// rows.
+__device__ __forceinline__ void fill_table(const GemmI8Args& a, int bm, int* table) {
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 64) {
+        const int e = e0 + lane;
+        int64_t lo = 0, hi = 0;
+        if (e < a.experts) {
+            lo = a.offsets[e];
+            hi = a.offsets[e + 1];
+            lo = lo < 0 ? 0 : lo > a.rows ? a.rows : lo;
+            hi = hi < lo ? lo : hi > a.rows ? a.rows : hi;
+        }
+        const int n = (int)((hi - lo + bm - 1) / bm);
+        int sum = n;
+        for (int d = 1; d < 64; d *= 2) {
+            const int x = __shfl_up(sum, d, 64);
+            if (lane >= d) sum += x;
+        }
+        if (e < a.experts) {
+            table[e] = before + sum - n;
+            table[a.experts + 1 + e] = (int)lo;
+            if (e == a.experts - 1) table[a.experts + 1 + a.experts] = (int)hi;
+        }
+        before += __shfl(sum, 63, 64);
+    }
+    if (lane == 0) table[a.experts] = before;
+}
+
+struct Tile {
+    int e, from, to;  // rows from .. to - 1 of expert e
+    int n0;
+};
+
+// v, of which the compiler does not know that it is the same every time: what
+// is worked out of it stays where it is used and holds no registers elsewhere.
+__device__ __forceinline__ int again(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Tile t of rtiles x ncols, in bands of four row tiles, so that what a die's L2
+// holds of both sides is used again.
+__device__ __forceinline__ Tile tile_at(const GemmI8Args& a, int t, int rtiles, int ncols, int bm, int bn, const int* table) {
+    constexpr int BAND = 4;
+    const int band = t / (BAND * ncols), first = band * BAND;
+    const int high = rtiles - first < BAND ? rtiles - first : BAND;
+    const int in = t - first * ncols, row = first + in % high;
+    Tile r;
+    r.n0 = (in / high) * bn;
+    if (!a.offsets) {
+        r.e = 0;
+        r.from = row * bm;
+        r.to = a.rows - r.from < bm ? (int)a.rows : r.from + bm;
+        return r;
+    }
+    // The last expert whose tiles begin at or before this one: 64 places
+    // apart, then among those between.
+    const int lane = threadIdx.x & 63, apart = (a.experts + 63) / 64;
+    const int far = lane * apart;
+    const uint64_t some = __ballot(far < a.experts && table[far < a.experts ? far : 0] <= row);
+    const int e0 = ((int)__popcll(some) - 1) * apart;
+    const int near = e0 + lane;
+    const uint64_t those = __ballot(lane < apart && near < a.experts && table[near < a.experts ? near : 0] <= row);
+    r.e = uniform(e0 + (int)__popcll(those) - 1);
+    r.from = uniform(table[a.experts + 1 + r.e] + (row - table[r.e]) * bm);
+    const int end = uniform(table[a.experts + 1 + r.e + 1]);  // the tile has rows, so it is not below the first one
+    r.to = end - r.from < bm ? end : r.from + bm;
+    return r;
+}
+
+// A wave's sums to memory.  Lane l of a 32 x 32 block holds columns
+// 8 b + 4 (l / 32) .. + 3 of row l % 32; scaled and rounded they go through LDS
+// (32 rows of 128 bytes, pieces swizzled as above), from where whole pieces of
+// rows leave 16 bytes a lane.
+constexpr int OUT = 32 * 128;  // bytes of LDS per wave
+
+template <typename T, int NF, int MF, bool GLU>
+__device__ __forceinline__ void store_block(const GemmI8Args& a, const Tile& t, int m0, int64_t c0, const float* sx,
+                                            const float* sg, const float* su, const i32x16 (&acc)[GLU ? 2 : 1][NF][MF],
+                                            unsigned char* lds) {
+    constexpr int FIT = 128 / (int)sizeof(T), COLS = FIT < 32 * NF ? FIT : 32 * NF;  // at a time
+    constexpr int PIECE = 16 / (int)sizeof(T), PIECES = COLS / PIECE;
+    static_assert(COLS % 32 == 0 && NF * 32 % COLS == 0, "whole blocks at a time");
+    typedef T vec4 __attribute__((ext_vector_type(4)));
+    const int lane = again(threadIdx.x & 63), r = lane & 31, h = lane >> 5;
+    const bool wide = a.n % PIECE == 0;
+    T* const y = static_cast<T*>(a.y);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-        const int row = 8 * (LOADS * wave + i) + (lane >> 3);
-        at_k[i] = 16 * slot_of(row, lane & 7);
-        if (row < BM) {
-            const int64_t p = rt.from + row;
-            const int64_t x = p < rt.to ? activation_row(a, p) : -1;
-            off[i] = x >= 0 ? (u32)x * (u32)a.k + (u32)at_k[i] : xbytes;
-        } else {
-            const int64_t j = n0 + (row - BM) % BN;
-            off[i] = j < a.n ? (u32)j * (u32)a.k + (u32)at_k[i] : wbytes;
+    for (int j = 0; j < MF; ++j) {
+        const int64_t p0 = (int64_t)t.from + m0 + 32 * j;
+        if (p0 >= t.to) break;
+        const float xs = sx[m0 + 32 * j + r];
+#pragma unroll
+        for (int i0 = 0; i0 < NF; i0 += COLS / 32) {
+#pragma unroll
+            for (int i = i0; i < i0 + COLS / 32; ++i)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int c = 32 * i + 8 * b + 4 * h;
+                    const f32x4 g = *reinterpret_cast<const f32x4*>(sg + c);
+                    f32x4 u;
+                    if constexpr (GLU) u = *reinterpret_cast<const f32x4*>(su + c);
+                    vec4 out;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        float s = (float)acc[0][i][j][4 * b + v] * xs * g[v];
+                        if constexpr (GLU) s = silu(s) * ((float)acc[1][i][j][4 * b + v] * xs * u[v]);
+                        out[v] = (T)s;
+                    }
+                    const int at = (c - 32 * i0) * (int)sizeof(T);
+                    *reinterpret_cast<vec4*>(lds + r * 128 + 16 * slot_of(r, at >> 4) + (at & 15)) = out;
+                }
+            if (wide) {
+#pragma unroll
+                for (int q0 = 0; q0 < 32 * PIECES; q0 += 64) {
+                    const int row = (q0 + lane) / PIECES, piece = (q0 + lane) % PIECES;
+                    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * 128 + 16 * slot_of(row, piece));
+                    const int64_t c = c0 + 32 * i0 + piece * PIECE;
+                    if (p0 + row < t.to && c < a.n) *reinterpret_cast<u32x4*>(y + (p0 + row) * a.n + c) = v;
+                }
+            } else {
+                for (int q = lane; q < 32 * COLS; q += 64) {
+                    const int row = q / COLS, at = q % COLS * (int)sizeof(T);
+                    const T v = *reinterpret_cast<const T*>(lds + row * 128 + 16 * slot_of(row, at >> 4) + (at & 15));
+                    const int64_t c = c0 + 32 * i0 + q % COLS;
+                    if (p0 + row < t.to && c < a.n) y[(p0 + row) * a.n + c] = v;
+                }
+            }
         }
     }
-    auto load = [&](int st) {
-        const u32 stage = (u32)(st & 1) * STAGE;
+}
+
+template <int WM, int WN, int MF, int NF, bool GLU>
+struct TileShape {
+    static constexpr int S = GLU ? 2 : 1, WAVES = WM * WN, T = 64 * WAVES;
+    static constexpr int BM = 32 * MF * WM, BN = 32 * NF * WN;  // columns of each stack
+    static constexpr int ROWS = BM + S * BN, STAGE = ROWS * BK;
+    static constexpr int LOADS = ROWS / 8 / WAVES;  // of one kilobyte, eight rows, per wave
+    static constexpr int SCALES = (ROWS + T - 1) / T;  // per thread
+    static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "a load brings rows of one side in all waves");
+    static_assert(BM <= T, "a thread for each row");
+    static_assert(WAVES * OUT <= STAGE, "outputs pass through a stage's place");
+};
+
+template <int WM, int WN, int MF, int NF, bool GLU, int OCC>
+__global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a) {
+    using Shape = TileShape<WM, WN, MF, NF, GLU>;
+    constexpr int S = Shape::S, BM = Shape::BM, BN = Shape::BN, ROWS = Shape::ROWS, STAGE = Shape::STAGE, LOADS = Shape::LOADS;
+    constexpr int T = Shape::T, SCALES = Shape::SCALES, WAVES = Shape::WAVES;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
+    __shared__ __attribute__((aligned(16))) float scales[2 * ROWS];  // of two tiles
+    __shared__ int rows_of[BM];
+    __shared__ int table[2 * (I8_EXPERTS + 1)];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int ncols = (int)((a.n + BN - 1) / BN);
+    int rtiles;
+    if (a.offsets) {
+        if (wave == 0) fill_table(a, BM, table);
+        __syncthreads();
+        rtiles = uniform(table[a.experts]);
+    } else {
+        rtiles = (int)((a.rows + BM - 1) / BM);
+    }
+    // Each of the 8 dies (work-group i runs on die i % 8) takes neighbouring tiles.
+    const int tiles = rtiles * ncols, per = (tiles + 7) / 8, base = (int)(blockIdx.x % 8) * per;
+    const int count = tiles - base < per ? tiles - base : per, hop = (int)(gridDim.x / 8);
+    int t = (int)(blockIdx.x / 8);
+    if (t >= count) return;
+
+    const u32 wbytes = (u32)(a.n * a.k), xbytes = (u32)(a.x_rows_count * a.k);
+    const int steps = (a.k + BK - 1) / BK;
+    // Load i of this wave brings the eight LDS rows from 8 (i WAVES + wave) on:
+    // first the activations', then the gate's (or the only) columns', then the
+    // up's.  Which of them is the same for all waves.
+    const auto lds_row = [&](int i) { return 8 * (i * WAVES + wave); };
+    const auto side = [](int i) constexpr { return 8 * i * WAVES < BM ? 0 : 8 * i * WAVES < BM + BN ? 1 : 2; };
+    const u32x4 xr = bounded_rsrc(a.x, xbytes);
+    // Activation row of row `tid` of a tile (-1: none); they wait in LDS.
+    const auto fetch_row = [&](const Tile& q) {
+        const int l = again(tid);
+        int x = l < BM && l < q.to - q.from ? (a.x_rows ? a.x_rows[q.from + l] : q.from + l) : -1;
+        return x < a.x_rows_count ? x : -1;
+    };
+    const auto fetch_scales = [&](const Tile& q, float (&s)[SCALES]) {
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int row = 8 * (LOADS * wave + i);  // of the first lane: one side for all of them
-            const u32 to = lds_address(lds + stage + row * BK);
-            // Behind K, and where there is no row, the load gives zeros.
-            const u32 end = row < BM ? xbytes : wbytes;
-            const u32 o = st * BK + at_k[i] < a.k && off[i] < end ? off[i] + (u32)(st * BK) : end;
-            if (row < BM)
-                load_to_lds(xr, o, to);
-            else if (row < BM + BN)
-                load_to_lds(wr, o, to);
-            else
-                load_to_lds(ur, o, to);
+        for (int i = 0; i < SCALES; ++i) {
+            const int at = again(tid) + i * T;
+            s[i] = __builtin_nanf("");  // no such activation row
+            if (at < BM) {
+                const int x = rows_of[at];
+                if (x >= 0) s[i] = a.xs[x];
+            } else if (at < ROWS) {
+                const int64_t c = (int64_t)q.n0 + (at - BM) % BN;
+                if (c < a.n) s[i] = (at < BM + BN ? a.ws : a.ws2)[(int64_t)q.e * a.n + c];
+            }
         }
     };
-    const int wm = wave % WM, wn = wave / WM;
-    const int r = lane & 31, h = lane >> 5;
-    i32x16 acc[S][NF][MF];
+    u32x4 wr, ur;
+    const auto offsets = [&](const Tile& q, u32 (&off)[LOADS]) {
+        const int64_t stack = (int64_t)q.e * a.n * a.k;
+        wr = bounded_rsrc(a.w + stack, wbytes);
+        ur = GLU ? bounded_rsrc(a.w2 + stack, wbytes) : wr;
 #pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int i = 0; i < NF; ++i)
-#pragma unroll
-            for (int j = 0; j < MF; ++j)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) acc[s][i][j][v] = 0;
-    const int steps = (a.k + BK - 1) / BK;
-    load(0);
-    for (int st = 0; st < steps; ++st) {
-        // The stage's loads, this wave's, are there, and what it read of the
-        // other stage too; behind the barrier everybody's.
-        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
-        asm volatile("s_barrier" ::: "memory");
-        if (st + 1 < steps) load(st + 1);
-        const unsigned char* base = lds + (st & 1) * STAGE;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            i32x4 w[S][NF], x[MF];
-#pragma unroll
-            for (int j = 0; j < MF; ++j) {
-                const int row = (wm * MF + j) * 32 + r;
-                x[j] = *reinterpret_cast<const i32x4*>(base + row * BK + 16 * slot_of(row, 2 * kk + h));
+        for (int i = 0; i < LOADS; ++i) {
+            const int me = again(lane), l = lds_row(i) + (me >> 3), at_k = 16 * slot_of(l, me & 7);
+            if (side(i) == 0) {
+                const int x = rows_of[l];
+                off[i] = x >= 0 ? (u32)x * (u32)a.k + (u32)at_k : xbytes;
+            } else {
+                const int64_t j = (int64_t)q.n0 + (l - BM) % BN;
+                off[i] = j < a.n ? (u32)j * (u32)a.k + (u32)at_k : wbytes;
             }
+        }
+    };
+    const auto load = [&](const u32 (&off)[LOADS], int st, int stage) {
 #pragma unroll
-            for (int s = 0; s < S; ++s)
+        for (int i = 0; i < LOADS; ++i) {
+            // Behind K, and where there is no row, the load gives zeros.
+            const u32 end = side(i) == 0 ? xbytes : wbytes;
+            const bool there = st * BK + 16 * slot_of(lds_row(i) + (lane >> 3), lane & 7) < a.k && off[i] < end;
+            load_to_lds(side(i) == 0 ? xr : side(i) == 1 ? wr : ur, there ? off[i] + (u32)(st * BK) : end,
+                        lds_address(lds + stage * STAGE + lds_row(i) * BK));
+        }
+    };
+    const auto keep_scales = [&](const float (&s)[SCALES], int which) {
 #pragma unroll
-                for (int i = 0; i < NF; ++i) {
-                    const int row = BM + s * BN + (wn * NF + i) * 32 + r;
-                    w[s][i] = *reinterpret_cast<const i32x4*>(base + row * BK + 16 * slot_of(row, 2 * kk + h));
-                }
+        for (int i = 0; i < SCALES; ++i)
+            if (tid + i * T < ROWS) scales[which * ROWS + tid + i * T] = s[i];
+    };
+    // (Waves of one row block on different SIMDs.)
+    const int wm = wave / WN, wn = wave % WN;
+    const int r = lane & 31, h = lane >> 5;
+    struct Pieces {
+        i32x4 w[S][NF], x[MF];
+    };
+    // Quarter kk (32 codes) of a stage.
+    const auto read = [&](Pieces& f, int stage, int kk) {
+        const unsigned char* from = lds + stage * STAGE;
+#pragma unroll
+        for (int j = 0; j < MF; ++j) {
+            const int row = (wm * MF + j) * 32 + r;
+            f.x[j] = *reinterpret_cast<const i32x4*>(from + row * BK + 16 * slot_of(row, 2 * kk + h));
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < NF; ++i) {
+                const int row = BM + s * BN + (wn * NF + i) * 32 + r;
+                f.w[s][i] = *reinterpret_cast<const i32x4*>(from + row * BK + 16 * slot_of(row, 2 * kk + h));
+            }
+    };
+
+    Tile cur = tile_at(a, base + t, rtiles, ncols, BM, BN, table);
+    u32 off[LOADS];
+    int stage = 0, which = 0;
+    {
+        float s[SCALES];
+        const int x = fetch_row(cur);
+        if (tid < BM) rows_of[tid] = x;
+        __syncthreads();
+        offsets(cur, off);
+        load(off, 0, 0);
+        fetch_scales(cur, s);
+        keep_scales(s, 0);
+    }
+    loads_barrier();
+    for (;;) {
+        i32x16 acc[S][NF][MF];
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int j = 0; j < MF; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[s][i][j][v] = 0;
+        const auto multiply = [&](const Pieces& f) {
 #pragma unroll
             for (int s = 0; s < S; ++s)
 #pragma unroll
                 for (int i = 0; i < NF; ++i)
 #pragma unroll
                     for (int j = 0; j < MF; ++j)
-                        acc[s][i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[s][i], x[j], acc[s][i][j], 0, 0, 0);
-        }
-    }
-    // Lane l of a 32 x 32 block holds columns 8 b + 4 (l / 32) .. + 3 of row l % 32.
-#pragma unroll
-    for (int j = 0; j < MF; ++j) {
-        const int64_t p = rt.from + (wm * MF + j) * 32 + r;
-        if (p >= rt.to) continue;
-        const int64_t x = activation_row(a, p);
-        const float xs = x >= 0 ? a.xs[x] : __builtin_nanf("");
-#pragma unroll
-        for (int i = 0; i < NF; ++i)
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                int g[4], u[4];
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    g[v] = acc[0][i][j][4 * b + v];
-                    u[v] = acc[S - 1][i][j][4 * b + v];
-                }
-                store4<GLU>(a, p, rt.e, n0 + (wn * NF + i) * 32 + 8 * b + 4 * h, xs, g, u);
+                        acc[s][i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[s][i], f.x[j], acc[s][i][j], 0, 0, 0);
+        };
+        const bool more = t + hop < count;
+        Tile next{};
+        int x = -1;
+        float s[SCALES];
+        if (more) {
+            next = tile_at(a, base + t + hop, rtiles, ncols, BM, BN, table);
+            x = fetch_row(next);
+            if (steps == 1) {
+                if (tid < BM) rows_of[tid] = x;
+                __syncthreads();
             }
+        }
+        // The next tile's first step.  (Not inside the loop: what it loads into
+        // registers would be waited for on every turn, and the stages with it.)
+        const auto bring_next = [&](int to) {
+            if (!more) return;
+            fetch_scales(next, s);
+            offsets(next, off);
+            load(off, 0, to);
+        };
+        if (steps > 1)
+            load(off, 1, stage ^ 1);
+        else
+            bring_next(stage ^ 1);
+        Pieces even, odd;
+        read(even, stage, 0);
+        const auto quarters = [&] {
+            read(odd, stage, 1);
+            multiply(even);
+            read(even, stage, 2);
+            multiply(odd);
+            read(odd, stage, 3);
+            multiply(even);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // Behind the barrier the other stage is there, and this one is read no more.
+        for (int st = 0; st + 2 < steps; ++st) {
+            quarters();
+            loads_barrier();
+            load(off, st + 2, stage);
+            stage ^= 1;
+            read(even, stage, 0);
+            multiply(odd);
+        }
+        if (steps > 1) {
+            quarters();
+            if (tid < BM) rows_of[tid] = x;
+            loads_barrier();
+            bring_next(stage);
+            stage ^= 1;
+            read(even, stage, 0);
+            multiply(odd);
+        }
+        quarters();
+        loads_barrier();
+        stage ^= 1;
+        multiply(odd);
+        if (more) keep_scales(s, which ^ 1);
+        unsigned char* const mine = lds + (stage ^ 1) * STAGE + wave * OUT;
+        const float* const sx = scales + which * ROWS;
+        const float* const sg = sx + BM + wn * NF * 32;
+        if (a.y16)
+            store_block<f16, NF, MF, GLU>(a, cur, wm * MF * 32, (int64_t)cur.n0 + wn * NF * 32, sx, sg, sg + BN, acc, mine);
+        else
+            store_block<float, NF, MF, GLU>(a, cur, wm * MF * 32, (int64_t)cur.n0 + wn * NF * 32, sx, sg, sg + BN, acc, mine);
+        if (!more) return;
+        lds_barrier();  // before the next step's loads go where the sums passed
+        cur = next;
+        t += hop;
+        which ^= 1;
     }
 }
 
@@ -334,28 +600,98 @@ hipError_t launch_rows(const GemmI8Args& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <int WM, int WN, int MF, int NF, bool GLU>
+template <int WM, int WN, int MF, int NF, bool GLU, int OCC>
 hipError_t launch_tile(const GemmI8Args& a, hipStream_t st) {
-    constexpr int BM = 32 * MF * WM, BN = 32 * NF * WN;
-    const int64_t grid = row_tiles(a, BM) * ((a.n + BN - 1) / BN);
-    if (grid > 0x7fffffff / (64 * WM * WN)) return hipErrorInvalidConfiguration;
-    tile_i8_kernel<WM, WN, MF, NF, GLU><<<dim3((unsigned)grid), dim3(64 * WM * WN), 0, st>>>(a);
+    using Shape = TileShape<WM, WN, MF, NF, GLU>;
+    const int64_t tiles = row_tiles(a, Shape::BM) * ((a.n + Shape::BN - 1) / Shape::BN);
+    if (tiles > 0x3fffffff) return hipErrorInvalidConfiguration;
+    // As many work-groups as the device holds at once, the same for every die.
+    int64_t grid = (int64_t)a.cus * std::max(1, 4 * OCC / Shape::WAVES) / 8 * 8;
+    if (grid > tiles) grid = (tiles + 7) / 8 * 8;
+    if (grid < 8) grid = 8;
+    tile_i8_kernel<WM, WN, MF, NF, GLU, OCC><<<dim3((unsigned)grid), dim3(Shape::T), 0, st>>>(a);
     return hipGetLastError();
+}
+
+// What a launch of a tile kernel takes, in microseconds, from timings of 84
+// dense shapes (1 to 1024 rows, 1000 to 16384 columns of 512 to 8192 codes) and
+// 44 grouped ones (16 and 128 experts): `begin` for a tile's ends and `one` for a
+// step of 128 codes while every tile has a compute unit for itself; `full` for a
+// step once all places are taken, and in proportion beyond.
+struct TileCost {
+    int bm, bn, places;  // work-groups that a compute unit holds
+    double begin, one, full;
+};
+constexpr TileCost COST_64{64, 64, 3, 2.5, 0.5, 0.85}, COST_64_GATED{64, 64, 2, 3.0, 0.85, 1.1};
+constexpr TileCost COST_128{128, 128, 2, 2.5, 0.72, 1.2}, COST_128_GATED{128, 64, 2, 2.5, 0.72, 1.2};
+constexpr TileCost COST_256{256, 256, 1, 5.0, 1.2, 1.78}, COST_256_GATED{256, 128, 1, 5.0, 1.2, 1.78};
+
+double tile_time(const GemmI8Args& a, const TileCost& c, double per, double met) {
+    // Grouped: every expert that has rows ends in a tile that is half empty on average.
+    const double rt = a.offsets ? std::max(met, per * a.experts / c.bm + met / 2) : (double)((a.rows + c.bm - 1) / c.bm);
+    const double tiles = rt * (double)((a.n + c.bn - 1) / c.bn), steps = (a.k + BK - 1) / BK;
+    const double alone = tiles / a.cus, rounds = alone / c.places;
+    if (rounds >= 1.0) return rounds * (c.begin + steps * c.full);
+    const double step = alone <= 1.0 && (c.places > 1 || alone <= 0.5) ? c.one : c.one + (c.full - c.one) * rounds;
+    return c.begin + steps * step;
+}
+
+template <bool GLU>
+hipError_t launch_few(const GemmI8Args& a, double per, hipStream_t st) {
+    if (a.offsets) {
+        // A row or a few for each expert: many work-groups, each with two waves
+        // for up to 1024 codes (128 experts, one row each, 2048 columns of 768:
+        // 26 us against 32 with four), four beyond (768 columns of 2048, gated: 39
+        // against 41 with two).  A second block of rows pays from about six rows on.
+        if (a.k <= 1024) return per <= 6 ? launch_rows<2, 1, 1, GLU>(a, st) : launch_rows<2, 1, 2, GLU>(a, st);
+        return per <= 6 ? launch_rows<4, 1, 1, GLU>(a, st) : launch_rows<4, 1, 2, GLU>(a, st);
+    }
+    // One matrix: all its rows in one work-group (16 MB of them), so weights are
+    // read once.  Eight waves share K, four where K is short or the columns
+    // alone fill the device (16384 columns of 4096, one row: 12.8 us against
+    // 14.9; 1024 of 8192: 9.8 against 7.2).  Twice the columns where that still fills it.
+    const bool many = a.n >= 32 * (int64_t)a.cus;
+    const bool short_k = a.k <= 2048 || a.n >= 64 * (int64_t)a.cus;
+    if (a.rows <= 16) return short_k ? launch_rows<4, 1, 1, GLU>(a, st) : launch_rows<8, 1, 1, GLU>(a, st);
+    if (a.rows <= 32) {
+        if (many) return launch_rows<4, 2, 2, GLU>(a, st);
+        return short_k ? launch_rows<4, 1, 2, GLU>(a, st) : launch_rows<8, 1, 2, GLU>(a, st);
+    }
+    if constexpr (!GLU) {
+        if (a.rows <= 48) return many ? launch_rows<8, 2, 3, false>(a, st) : launch_rows<8, 1, 3, false>(a, st);
+    }
+    // Blocks of 32 rows, where columns alone would leave most of the device idle
+    // (96 rows, 1024 columns of 8192: 13.5 us against 30 in tiles of 64).
+    const int64_t blocks = (a.rows + 31) / 32;
+    return blocks * a.n <= 32 * (int64_t)a.cus ? launch_rows<8, 1, 2, GLU>(a, st) : launch_rows<8, 2, 2, GLU>(a, st);
+}
+
+template <bool GLU>
+hipError_t launch_plan(const GemmI8Args& a, hipStream_t st) {
+    const double per = (double)a.rows / std::max(1, a.offsets ? a.experts : 1);
+    // Few rows for each matrix: bound by its bytes, the kernel without LDS stages.
+    // Grouped, up to where tiles of 128 are as fast (128 experts, gated: 8 rows
+    // each; plain: 6).  One matrix: while its blocks do not fill the device twice.
+    const int64_t blocks = (a.rows + 31) / 32;
+    const bool few = a.offsets ? per <= (GLU ? 9.0 : 6.0)
+                               : a.rows <= 48 || (a.rows <= 128 && blocks * a.n <= 64 * (int64_t)a.cus);
+    if (few) return launch_few<GLU>(a, per, st);
+    // Experts that have rows: all but those that chance leaves out.
+    const double met = a.offsets ? a.experts * (1.0 - std::exp(-per)) : 1.0;
+    const double t64 = tile_time(a, GLU ? COST_64_GATED : COST_64, per, met);
+    const double t128 = tile_time(a, GLU ? COST_128_GATED : COST_128, per, met);
+    const double t256 = tile_time(a, GLU ? COST_256_GATED : COST_256, per, met);
+    if (t64 <= t128 && t64 <= t256) return launch_tile<2, 2, 1, 1, GLU, GLU ? 2 : 3>(a, st);
+    if constexpr (GLU)
+        return t128 <= t256 ? launch_tile<4, 2, 1, 1, true, 4>(a, st) : launch_tile<4, 4, 2, 1, true, 4>(a, st);
+    else
+        return t128 <= t256 ? launch_tile<2, 4, 2, 1, false, 4>(a, st) : launch_tile<4, 4, 2, 2, false, 4>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t st) {
-    // Rows that a matrix meets.
-    const int64_t per = a.offsets ? (a.rows + a.experts - 1) / a.experts : a.rows;
-    if (a.w2) {
-        if (per <= 16) return launch_rows<8, 1, 1, true>(a, st);
-        if (per <= 64) return launch_rows<8, 1, 2, true>(a, st);
-        return launch_tile<2, 2, 2, 1, true>(a, st);
-    }
-    if (per <= 16) return launch_rows<8, 1, 1, false>(a, st);
-    if (per <= 64) return launch_rows<8, 1, 4, false>(a, st);
-    return launch_tile<2, 2, 2, 2, false>(a, st);
+    return a.w2 ? launch_plan<true>(a, st) : launch_plan<false>(a, st);
 }
 
 }  // namespace qmm

@@ -30,7 +30,7 @@ qmm_status check_i8(int64_t x_rows_count, int64_t p_rows, int64_t n_experts, int
     CHECK(n >= 0 && p_rows >= 0 && x_rows_count >= 0, QMM_ERR_INVALID_ARGUMENT, "n=%lld, rows=%lld or %lld is negative",
           (long long)n, (long long)p_rows, (long long)x_rows_count);
     CHECK(n_experts >= 0, QMM_ERR_INVALID_ARGUMENT, "n_experts=%lld is negative", (long long)n_experts);
-    CHECK(n_experts <= 65536, QMM_ERR_UNSUPPORTED, "n_experts=%lld above 65536", (long long)n_experts);
+    CHECK(n_experts <= I8_EXPERTS, QMM_ERR_UNSUPPORTED, "n_experts=%lld above %d", (long long)n_experts, I8_EXPERTS);
     CHECK(k >= 32 && k % 32 == 0, QMM_ERR_INVALID_ARGUMENT, "k=%lld must be a positive multiple of 32", (long long)k);
     CHECK(k <= 32768, QMM_ERR_UNSUPPORTED, "k=%lld above 32768", (long long)k);
     CHECK(n < FOUR_GIB / k, QMM_ERR_UNSUPPORTED, "one matrix of %lld x %lld codes is 4 GiB or more", (long long)n, (long long)k);

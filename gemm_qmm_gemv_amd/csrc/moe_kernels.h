@@ -46,6 +46,8 @@ struct QuantizeArgs {
 };
 hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t st);
 
+// Experts of one call at most.
+constexpr int I8_EXPERTS = 1024;
 struct GemmI8Args {
     const int8_t *w, *w2;        // [experts][n][k]; w2: the up stack of a gated product, or null
     const float *ws, *ws2;       // [experts][n]

@@ -84,6 +84,68 @@ def test_larger(m, n, k):
     dense(m, n, k, True)
 
 
+def on_device(x, xs, w, ws):
+    """float64 [rows][n] on the GPU: sums below 2^53 are exact."""
+    return (x.double() @ w.double().T) * xs.double()[:, None] * ws.double()[None, :]
+
+
+@pytest.mark.parametrize("m,n,k,f16", [(4096, 4096, 256, True), (4099, 5001, 160, False), (2500, 16384, 128, True), (1000, 8192, 512, False),
+                                       (520, 4096, 2048, True), (300, 16384, 96, False), (8192, 2048, 32, True)])
+def test_many_tiles(m, n, k, f16):
+    # Every tile size, several tiles for each work-group, one and more steps of K.
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m)
+    announce("gemm_i8 many tiles", m, n, k)
+    w = torch.randint(-128, 128, (n, k), device="cuda", dtype=torch.int8, generator=g)
+    x = torch.randint(-128, 128, (m, k), device="cuda", dtype=torch.int8, generator=g)
+    ws, xs = torch.rand(n, device="cuda", generator=g) * 1e-4, torch.rand(m, device="cuda", generator=g)
+    y = torch.full((m + 1, n), 77.0, dtype=torch.float16 if f16 else torch.float32, device="cuda")
+    qmm.qmm_gemm_i8(w, ws, x, xs, y, f16, m, n, k)
+    torch.cuda.synchronize()
+    assert (y[m] == 77).all()
+    want = on_device(x, xs, w, ws)
+    bound = 3.01 * E32 * want.abs() + (E16 * 1.01 * want.abs() + TINY16 if f16 else 0) + 1e-40
+    assert ((y[:m].double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("experts,n,k,mean", [(3, 1000, 160, 700), (40, 512, 96, 90), (128, 520, 64, 30), (2, 2048, 128, 3000), (8, 768, 2048, 500), (100, 256, 32, 200)])
+def test_many_grouped_tiles(glu, experts, n, k, mean):
+    rng = np.random.default_rng(experts)
+    counts = rng.integers(0, 2 * mean + 1, experts)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    p = int(offsets[-1])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(experts)
+    announce("moe_i8 many tiles", experts, p, n, k, "glu" if glu else "")
+    xr = p // 2 + 1
+    w = torch.randint(-128, 128, (experts, n, k), device="cuda", dtype=torch.int8, generator=g)
+    w2 = torch.randint(-128, 128, (experts, n, k), device="cuda", dtype=torch.int8, generator=g)
+    x = torch.randint(-128, 128, (xr, k), device="cuda", dtype=torch.int8, generator=g)
+    ws, ws2 = torch.rand((experts, n), device="cuda", generator=g) * 1e-4, torch.rand((experts, n), device="cuda", generator=g) * 1e-4
+    xs = torch.rand(xr, device="cuda", generator=g)
+    rows = torch.randint(0, xr, (p,), device="cuda", dtype=torch.int32, generator=g)
+    y = torch.full((p + 1, n), 77.0, device="cuda")
+    off = dev(offsets.astype(np.int32))
+    if glu:
+        qmm.qmm_moe_swiglu_i8(w, ws, w2, ws2, x, xs, rows, xr, off, y, False, p, experts, n, k)
+    else:
+        qmm.qmm_moe_gemm_i8(w, ws, x, xs, rows, xr, off, y, False, p, experts, n, k)
+    torch.cuda.synchronize()
+    assert (y[p] == 77).all()
+    for e in range(experts):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        at = rows[a:b].long()
+        v = on_device(x[at], xs[at], w[e], ws[e])
+        bound = 3.01 * E32 * v.abs() + 1e-40
+        if glu:
+            u = on_device(x[at], xs[at], w2[e], ws2[e])
+            h = v * torch.sigmoid(v) * u
+            bound = E32 * h.abs() * (3 * (1 + v.abs()) + 11) + 1e-35 * u.abs() + 1e-40
+            v = h
+        assert ((y[a:b].double() - v).abs() <= bound).all(), e
+
+
 def test_scales_that_are_not_finite_stay_in_their_rows_and_columns():
     rng = np.random.default_rng(9)
     for m, n in ((3, 50), (40, 50), (200, 90)):
