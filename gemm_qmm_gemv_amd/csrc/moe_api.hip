@@ -132,7 +132,7 @@ qmm_status qmm_moe_route(const void* logits, int logits_fp16, int64_t logits_str
     a.offsets = expert_offsets;
     a.pair_token = pair_token;
     a.pair_weight = pair_weight;
-    a.counts = static_cast<uint16_t*>(workspace);
+    a.counts = static_cast<uint8_t*>(workspace);
     a.stride = tokens > 1 ? logits_stride : 0;
     a.tokens = tokens;
     a.experts = n_experts;

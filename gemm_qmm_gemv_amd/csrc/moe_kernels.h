@@ -13,9 +13,6 @@ namespace qmm {
 // Sets the calling thread's qmm_last_error text and returns st (qmm_api.hip).
 qmm_status report(qmm_status st, const char* fmt, ...);
 
-// Tokens that one work-group routes when several share the work; its ranks
-// within an expert are counted in one 64-bit mask.
-constexpr int ROUTE_BLOCK = 64;
 struct RouteArgs {
     const void* logits;  // fp32 or fp16 rows
     const float* bias;   // or null
@@ -26,13 +23,12 @@ struct RouteArgs {
     int32_t* offsets;    // null: no grouping
     int32_t* pair_token;
     float* pair_weight;
-    uint16_t* counts;    // workspace [work-groups][experts rounded up to 8]
+    uint8_t* counts;     // workspace: rows of experts rounded up to 16
     int64_t stride, tokens;
     int experts, groups, top_groups, group_best, top_k;
     float scale;
     bool f16, sigmoid, renorm, vec;
 };
-bool route_in_one(int64_t tokens);
 size_t route_workspace(int64_t tokens, int experts);
 hipError_t launch_route(const RouteArgs& a, hipStream_t st);
 

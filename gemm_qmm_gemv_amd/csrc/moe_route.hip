@@ -12,6 +12,8 @@
 // logits, which are compared as they are; with one, scores are formed in 64
 // bits.  Keys are whole numbers in the order of the values, so that a place that
 // is taken (or not there) has a key below all of them.
+#include <type_traits>
+
 #include "layer_device.h"
 #include "moe_kernels.h"
 
@@ -19,6 +21,13 @@ namespace qmm {
 namespace {
 
 constexpr float INF = __builtin_huge_valf();
+// Tokens that one work-group routes and places in one launch: what it holds at
+// once, with a wave or 16 lanes for each.
+constexpr int ROUTE_ONE = 16, ROUTE_ONE_16 = 64;
+// Up to this many tokens get a wave each, and a work-group takes 16 of them.
+constexpr int ROUTE_WAVES = 4096;
+// Rows of counts that are summed up for the second launch, if there are more.
+constexpr int CHUNK = 64, CHUNKED = 256;
 
 __device__ __forceinline__ int order_key(float v) {
     const int b = __builtin_bit_cast(int, v + 0.f);  // -0 is 0
@@ -47,16 +56,24 @@ __device__ __forceinline__ V lane_move(V v) {
         return __builtin_bit_cast(V, r);
     }
 }
-template <class V>
-__device__ __forceinline__ V lane_xor(V v, int mask) {
+// f of v in lanes l and l ^ 16 (HALVES: l ^ 32), in both.
+template <bool HALVES, class V, class F>
+__device__ __forceinline__ V across(V v, F f) {
+    const auto swap = [](u32 x) {
+        if constexpr (HALVES)
+            return __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        else
+            return __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    };
     if constexpr (sizeof(V) == 4) {
-        return __builtin_bit_cast(V, __shfl_xor(__builtin_bit_cast(int, v), mask, 64));
+        const auto r = swap(__builtin_bit_cast(u32, v));
+        const u32 a = r[0], b = r[1];
+        return f(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b));
     } else {
         const u32x2 x = __builtin_bit_cast(u32x2, v);
-        u32x2 r;
-        r[0] = (u32)__shfl_xor((int)x[0], mask, 64);
-        r[1] = (u32)__shfl_xor((int)x[1], mask, 64);
-        return __builtin_bit_cast(V, r);
+        const auto lo = swap(x[0]), hi = swap(x[1]);
+        const u32x2 a = {(u32)lo[0], (u32)hi[0]}, b = {(u32)lo[1], (u32)hi[1]};
+        return f(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b));
     }
 }
 template <int N, class V, class F>
@@ -67,10 +84,26 @@ __device__ __forceinline__ V lanes(V v, F f) {
     v = f(v, lane_move<0x141>(v));
     v = f(v, lane_move<0x140>(v));
     if constexpr (N == 64) {
-        v = f(v, lane_xor(v, 16));
-        v = f(v, lane_xor(v, 32));
+        v = across<false>(v, f);
+        v = across<true>(v, f);
     }
     return v;
+}
+// v of the first lane for which `here` holds; none: `other`.  Lanes hold what
+// lies behind each other, so the first is the lowest index.
+template <int N, class V>
+__device__ __forceinline__ V first_of(bool here, V v, V other) {
+    static_assert(sizeof(V) == 4, "one register");
+    if constexpr (N == 64) {
+        const uint64_t who = __ballot(here);
+        if (who == 0) return other;
+        return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), __ffsll((unsigned long long)who) - 1));
+    } else {
+        const u32 who = (u32)(__ballot(here) >> (threadIdx.x & 48)) & 0xffffu;
+        const int from = (int)(threadIdx.x & 48) + __ffs(who) - 1;
+        const int r = __builtin_amdgcn_ds_bpermute(4 * from, __builtin_bit_cast(int, v));
+        return who ? __builtin_bit_cast(V, r) : other;
+    }
 }
 struct Max {
     template <class V>
@@ -85,6 +118,34 @@ struct Add {
     __device__ V operator()(V a, V b) const { return a + b; }
 };
 
+// Logits e0 .. e0 + PER - 1 of a token, -inf behind the last expert.
+template <int PER>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t token, int e0, float (&l)[PER]) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) l[i] = -INF;
+    const auto take_from = [&](auto p) {
+        if (a.vec && PER % 4 == 0) {
+            typedef std::remove_cv_t<std::remove_reference_t<decltype(*p)>> F;
+            typedef F vec __attribute__((ext_vector_type(4)));
+#pragma unroll
+            for (int i = 0; i < PER / 4 * 4; i += 4) {
+                if (e0 + i >= a.experts) continue;  // their number is a multiple of 4
+                const vec v = *reinterpret_cast<const vec*>(p + e0 + i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) l[i + j] = (float)v[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (e0 + i < a.experts) l[i] = (float)p[e0 + i];
+        }
+    };
+    if (a.f16)
+        take_from(static_cast<const f16*>(a.logits) + token * a.stride);
+    else
+        take_from(static_cast<const float*>(a.logits) + token * a.stride);
+}
+
 // What one token's lanes know after its choice: lane j < top_k holds expert and
 // weight of choice j.
 struct Chosen {
@@ -92,25 +153,216 @@ struct Chosen {
     float w;
 };
 
-// L lanes share a token; lane i of them holds experts i PER .. i PER + PER - 1.
+// Whether two scores in fp32 (with a bias, or sums of two) are so far apart that
+// those in 64 bits are in the same order: `near`, what the scores themselves may
+// be off by, and 2^-24 of their size for the bias and the sum, each at either side.
+__device__ __forceinline__ bool apart(float high, float low, float near) {
+    return high - low > near + 0x1p-22f * (fabsf(high) + fabsf(low));
+}
+
+// Of the lanes' groups of keys the `count` highest, the lower index first among
+// equals: lane j gets the index and the key of choice j.  Returns whether every
+// key chosen is apart from the next (the first left out included), if asked.
+template <int L, int PER, bool APART, class Key>
+__device__ __forceinline__ bool take(Key (&key)[PER], int e0, int lane, int count, int& id, Key& value, float near = 0.f) {
+    bool clear = true;
+    float before = 0.f;
+    for (int j = 0; j < count + (APART ? 1 : 0); ++j) {
+        Key m = key[0];
+#pragma unroll
+        for (int i = 1; i < PER; ++i) m = key[i] > m ? key[i] : m;
+        const Key best = lanes<L>(m, Max{});
+        if constexpr (APART) {
+            if (best != taken<Key>()) {
+                const float v = key_value(best);
+                if (j > 0) clear = clear && apart(before, v, near);
+                before = v;
+            }
+            if (j == count) break;
+        }
+        int at = e0;
+#pragma unroll
+        for (int i = PER - 1; i > 0; --i)
+            if (key[i] == best) at = e0 + i;
+        if (key[0] == best) at = e0;
+        const int e = first_of<L>(m == best, at, 0);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (e - e0 == i) key[i] = taken<Key>();
+        if (lane == j) {
+            id = e;
+            value = best;
+        }
+    }
+    return clear;
+}
+
+// The two highest of v's values among this lane's, then among the lanes' that
+// share a group.
+struct TwoBest {
+    template <class V>
+    __device__ static void add(V& x, V& y, V a) {
+        const V low = a < x ? a : x;
+        y = y > low ? y : low;
+        x = x > a ? x : a;
+    }
+};
+template <int CTRL, class V>
+__device__ __forceinline__ void join_two(V& x, V& y) {
+    const V a = lane_move<CTRL>(x), b = lane_move<CTRL>(y);
+    TwoBest::add(x, y, a);
+    y = y > b ? y : b;
+}
+
+// Keys of experts outside the top_groups best groups become taken.  v: what is
+// compared (its order is that of the keys); s: what is summed, if two are.
+// Returns whether the last group that stays and the first that does not are
+// apart, if asked.
+template <int L, int PER, bool APART, class Key, class V>
+__device__ __forceinline__ bool keep_groups(const RouteArgs& a, Key (&key)[PER], const V (&s)[PER], int e0, int lane, float near = 0.f) {
+    const int each = a.experts / a.groups;
+    const V low = -(V)INF;
+    bool clear = true;
+    using Mark = std::conditional_t<sizeof(Key) == 4 && sizeof(V) == 4, int, int64_t>;
+    Mark mine = taken<Mark>();  // the score of the lane's group, in the first lane of it
+    int group = lane;
+    const int wide = each / PER;  // lanes of a group
+    if (each % PER == 0 && wide <= 8 && (wide & (wide - 1)) == 0) {
+        // Every lane's experts are of one group: all groups at once.
+        group = e0 / each;
+        if (a.group_best == 1) {
+            Key k = key[0];
+#pragma unroll
+            for (int i = 1; i < PER; ++i) k = key[i] > k ? key[i] : k;
+            if (wide >= 2) k = Max{}(k, lane_move<0xB1>(k));
+            if (wide >= 4) k = Max{}(k, lane_move<0x4E>(k));
+            if (wide >= 8) k = Max{}(k, lane_move<0x141>(k));
+            mine = k;
+        } else {
+            V x = low, y = low;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) TwoBest::add(x, y, s[i]);
+            if (wide >= 2) join_two<0xB1>(x, y);
+            if (wide >= 4) join_two<0x4E>(x, y);
+            if (wide >= 8) join_two<0x141>(x, y);
+            V sum = x + y;
+            if (sum != sum) sum = low;
+            mine = order_key(sum);
+        }
+        if (lane % wide != 0 || e0 >= a.experts) mine = taken<Mark>();
+    } else {
+        // One group after the other, over all lanes.
+        for (int g = 0; g < a.groups; ++g) {
+            const int lo = g * each, hi = lo + each;
+            if (a.group_best == 1) {
+                Key k = taken<Key>();
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (e0 + i >= lo && e0 + i < hi && key[i] > k) k = key[i];
+                k = lanes<L>(k, Max{});
+                if (lane == g) mine = k;
+            } else {
+                V x = low, y = low;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (e0 + i >= lo && e0 + i < hi) TwoBest::add(x, y, s[i]);
+                const V first = lanes<L>(x, Max{});
+                const int owner = first_of<L>(x == first, lane, L);
+                V sum = first + lanes<L>(lane == owner ? y : x, Max{});
+                if (sum != sum) sum = low;
+                if (lane == g) mine = order_key(sum);
+            }
+        }
+    }
+    // One bit for each group that stays.
+    uint64_t stay = 0;
+    float last = 0.f;
+    for (int j = 0; j < a.top_groups + (APART ? 1 : 0); ++j) {
+        const Mark m = lanes<L>(mine, Max{});
+        if (m == taken<Mark>()) break;
+        if constexpr (APART) {
+            // (The order among those that stay is of no account.)
+            const float v = key_value(m);
+            if (j == a.top_groups) {
+                clear = apart(last, v, a.group_best == 2 ? 2.f * near : near);
+                break;
+            }
+            last = v;
+        }
+        const int owner = first_of<L>(mine == m, lane, 0), g = first_of<L>(mine == m, group, 0);
+        stay |= 1ull << g;
+        if (lane == owner) mine = taken<Mark>();
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = e0 + i;
+        if (e < a.experts && !(stay >> (e / each) & 1)) key[i] = taken<Key>();
+    }
+    return clear;
+}
+
+// The choice on scores in 64 bits.
 template <int L, int PER, bool BIAS>
-__device__ __forceinline__ Chosen choose(const RouteArgs& a, int64_t token, int lane) {
-    using Key = std::conditional_t<BIAS, int64_t, int>;
+__device__ __forceinline__ int choose_exact(const RouteArgs& a, int64_t token, float top, int lane) {
     const int e0 = lane * PER;
     float l[PER];
+    load_logits<PER>(a, token, e0, l);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) l[i] = -INF;
-    if (a.f16) {
-        const f16* p = static_cast<const f16*>(a.logits) + token * a.stride;
+    for (int i = 0; i < PER; ++i)
+        if (l[i] != l[i]) l[i] = -INF;
+    double s[PER];
+    if (a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (e0 + i < a.experts) l[i] = (float)p[e0 + i];
+        for (int i = 0; i < PER; ++i) s[i] = 1.0 / (1.0 + exp(-(double)l[i]));
     } else {
-        const float* p = static_cast<const float*>(a.logits) + token * a.stride;
+        double sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (e0 + i < a.experts) l[i] = p[e0 + i];
+        for (int i = 0; i < PER; ++i) {
+            s[i] = top == -INF ? 0.0 : l[i] == top ? 1.0 : exp((double)l[i] - (double)top);  // top may be +inf
+            sum += s[i];
+        }
+        sum = lanes<L>(sum, Add{});
+        const double r = sum > 0.0 ? 1.0 / sum : 0.0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) s[i] *= r;
     }
+    int id = -1;
+    if constexpr (BIAS) {
+        int64_t key[PER], best = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (e0 + i < a.experts) s[i] += (double)a.bias[e0 + i];
+            if (s[i] != s[i] || e0 + i >= a.experts) s[i] = -(double)INF;
+            key[i] = e0 + i < a.experts ? order_key(s[i]) : taken<int64_t>();
+        }
+        if (a.groups > 1) keep_groups<L, PER, false>(a, key, s, e0, lane);
+        take<L, PER, false>(key, e0, lane, a.top_k, id, best);
+    } else {
+        int key[PER], best = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            key[i] = e0 + i < a.experts ? order_key(l[i]) : taken<int>();
+            if (e0 + i >= a.experts) s[i] = -(double)INF;
+        }
+        if (a.groups > 1) keep_groups<L, PER, false>(a, key, s, e0, lane);
+        take<L, PER, false>(key, e0, lane, a.top_k, id, best);
+    }
+    return id;
+}
+
+// What a choice is made on.
+enum Mode {
+    LOGITS,  // the logits: their order is the scores'
+    PAIRS,   // the same, in groups by the sum of their two best scores
+    BIASED,  // scores and biases
+};
+
+// L lanes share a token; lane i of them holds experts i PER .. i PER + PER - 1.
+template <int L, int PER, Mode MODE>
+__device__ __forceinline__ Chosen choose(const RouteArgs& a, int64_t token, int lane) {
+    const int e0 = lane * PER;
+    float l[PER];
+    load_logits<PER>(a, token, e0, l);
     // A NaN is placed as -inf and makes the token's weights NaN.
     int bad = 0;
     float top = -INF;
@@ -127,113 +379,63 @@ __device__ __forceinline__ Chosen choose(const RouteArgs& a, int64_t token, int 
     if (!a.sigmoid && top == INF) bad = 1;
     const bool empty = top == -INF;  // every score is zero
 
-    const bool pairs = a.groups > 1 && a.group_best == 2;
-    double s[PER];  // scores in 64 bits where a sum of them is compared
-    if (BIAS || pairs) {
+    constexpr bool BIAS = MODE == BIASED;
+    int key[PER], best = 0;
+    Chosen c{-1, 0.f};
+    float sum_all = 0.f;
+    if constexpr (MODE == LOGITS) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = e0 + i < a.experts ? order_key(l[i]) : taken<int>();
+        if (a.groups > 1) keep_groups<L, PER, false>(a, key, l, e0, lane);
+        take<L, PER, false>(key, e0, lane, a.top_k, c.id, best);
+    } else {
+        // In fp32 first; where that leaves a choice open, in 64 bits.  A sigmoid
+        // is good to 2^-22 (exponential and quotient), a softmax score p to 2^-19
+        // p (and at most 22 additions); near is that of two, and twice as much.
+        float s[PER], near = 0x1p-20f;
         if (a.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) s[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+            for (int i = 0; i < PER; ++i) s[i] = 1.f / (1.f + expf(-l[i]));
         } else {
-            double sum = 0.0;
+            float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                s[i] = empty ? 0.0 : l[i] == top ? 1.0 : exp((double)l[i] - (double)top);  // top may be +inf
+                s[i] = empty ? 0.f : expf(l[i] - top);
                 sum += s[i];
             }
-            sum = lanes<L>(sum, Add{});
-            const double r = empty ? 0.0 : 1.0 / sum;
+            sum_all = lanes<L>(sum, Add{});
+            const float r = empty ? 0.f : 1.f / sum_all;
+            near = 0x1p-17f * r;  // r is the largest score
 #pragma unroll
             for (int i = 0; i < PER; ++i) s[i] *= r;
         }
-        if constexpr (BIAS) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (e0 + i < a.experts) s[i] += (double)a.bias[e0 + i];
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (s[i] != s[i]) s[i] = -(double)INF;
-    }
-    Key key[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        if constexpr (BIAS)
-            key[i] = order_key(s[i]);
-        else
-            key[i] = order_key(l[i]);
-        if (e0 + i >= a.experts) key[i] = taken<Key>();
-    }
-    if (a.groups > 1) {
-        const int each = a.experts / a.groups;
-        // Lane g holds the score of group g.
-        int64_t mine = taken<int64_t>();
-        for (int g = 0; g < a.groups; ++g) {
-            const int lo = g * each, hi = lo + each;
-            int64_t best;
-            if (a.group_best == 1) {
-                Key k = taken<Key>();
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    if (e0 + i >= lo && e0 + i < hi && key[i] > k) k = key[i];
-                best = lanes<L>(k, Max{});
-            } else {
-                // The two highest, lane by lane and then over the lanes.
-                double x = -(double)INF, y = -(double)INF;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    if (e0 + i < lo || e0 + i >= hi) continue;
-                    y = fmax(y, fmin(x, s[i]));
-                    x = fmax(x, s[i]);
-                }
-                const double first = lanes<L>(x, Max{});
-                const int owner = lanes<L>(x == first ? lane : L, Min{});
-                const double second = lanes<L>(lane == owner ? y : x, Max{});
-                double sum = first + second;
-                if (sum != sum) sum = -(double)INF;
-                best = order_key(sum);
-            }
-            if (lane == g) mine = best;
-        }
-        // One bit for each group that stays.
-        uint64_t stay = 0;
-        for (int j = 0; j < a.top_groups; ++j) {
-            const int64_t m = lanes<L>(mine, Max{});
-            const int g = lanes<L>(mine == m ? lane : L, Min{});
-            stay |= 1ull << g;
-            if (lane == g) mine = taken<int64_t>();
-        }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = e0 + i;
-            if (e < a.experts && !(stay >> (e / each) & 1)) key[i] = taken<Key>();
-        }
-    }
-    Chosen c{-1, 0.f};
-    float chosen_l = -INF;
-    for (int j = 0; j < a.top_k; ++j) {
-        Key m = key[0];
-        int at = e0;
-#pragma unroll
-        for (int i = 1; i < PER; ++i)
-            if (key[i] > m) {
-                m = key[i];
-                at = e0 + i;
+            if constexpr (BIAS) {
+                if (e0 + i < a.experts) s[i] += a.bias[e0 + i];
+                if (s[i] != s[i]) s[i] = -INF;
+                key[i] = order_key(s[i]);
+            } else {
+                key[i] = order_key(l[i]);
             }
-        const Key best = lanes<L>(m, Max{});
-        const int e = lanes<L>(m == best ? at : 0x7fffffff, Min{});
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (e0 + i == e) key[i] = taken<Key>();
-        if (lane == j) {
-            c.id = e;
-            if constexpr (!BIAS) chosen_l = key_value(best);
+            if (e0 + i >= a.experts) {
+                s[i] = -INF;
+                key[i] = taken<int>();
+            }
+        }
+        bool clear = true;
+        if (a.groups > 1) clear = keep_groups<L, PER, true>(a, key, s, e0, lane, near);
+        clear = take<L, PER, BIAS>(key, e0, lane, a.top_k, c.id, best, near) && clear;
+        if (__any(!clear)) {
+            const int id = choose_exact<L, PER, BIAS>(a, token, top, lane);
+            if (!clear) c.id = id;
         }
     }
-    if constexpr (BIAS) {
-        if (lane < a.top_k) {
-            const int64_t at = token * a.stride + c.id;
-            chosen_l = a.f16 ? (float)static_cast<const f16*>(a.logits)[at] : static_cast<const float*>(a.logits)[at];
-        }
+    float chosen_l = -INF;
+    if (lane < a.top_k) {
+        const int64_t at = token * a.stride + c.id;
+        chosen_l = a.f16 ? (float)static_cast<const f16*>(a.logits)[at] : static_cast<const float*>(a.logits)[at];
+        if (chosen_l != chosen_l) chosen_l = -INF;
     }
     // Weights from the logits of the chosen, in fp32.
     float w = 0.f;
@@ -252,10 +454,17 @@ __device__ __forceinline__ Chosen choose(const RouteArgs& a, int64_t token, int 
             w = sum > 0.f ? w / sum : 0.f;
         }
     } else if (!empty) {
-        if (lane < a.top_k) w = expf(chosen_l - top);
-        float sum;
+        // Where only ratios count, from the largest of the chosen.
+        float from = top, sum;
+        if (a.renorm) {
+            from = lanes<L>(lane < a.top_k ? chosen_l : -INF, Max{});
+            if (from == -INF) from = top;
+        }
+        if (lane < a.top_k) w = expf(chosen_l - from);
         if (a.renorm) {
             sum = lanes<L>(w, Add{});
+        } else if constexpr (MODE != LOGITS) {
+            sum = sum_all;
         } else {
             sum = 0.f;
 #pragma unroll
@@ -268,133 +477,208 @@ __device__ __forceinline__ Chosen choose(const RouteArgs& a, int64_t token, int 
     return c;
 }
 
-// A work-group takes ROUTE_BLOCK tokens (ONE: all of them, in as many rounds)
-// and T / L of them at a time.  Ranks within an expert come from a mask per
-// expert with a bit for each token: a token names an expert at most once.
-template <int T, int L, int PER, bool BIAS, bool ONE>
-__global__ void __launch_bounds__(T) route_kernel(RouteArgs a) {
-    extern __shared__ uint64_t mask[];  // [experts], then ids and weights of the block's pairs
-    __shared__ int part[T / 64];
-    constexpr int TOKENS = T / L;
-    const int tid = threadIdx.x, lane = tid % L, slot = tid / L;
+// Sums over the experts before, T of them at a time, in all threads of a
+// work-group: to(e, sum before, own) for each expert, the sum of all returned.
+template <class N, class To>
+__device__ __forceinline__ int sums_before(int experts, int* part, N own, To to) {
+    const int tid = threadIdx.x, threads = blockDim.x;
+    int base = 0;
+    for (int e0 = 0; e0 < experts; e0 += threads) {
+        const int e = e0 + tid, n = e < experts ? own(e) : 0;
+        int sum = n;
+        for (int d = 1; d < 64; d *= 2) {
+            const int before = __shfl_up(sum, d, 64);
+            if ((tid & 63) >= d) sum += before;
+        }
+        if ((tid & 63) == 63) part[tid >> 6] = sum;
+        __syncthreads();
+        int before = base;
+        for (int i = 0; i < threads / 64; ++i) {
+            if (i < tid >> 6) before += part[i];
+            base += part[i];
+        }
+        if (e < experts) to(e, before + sum - n, n);
+        __syncthreads();
+    }
+    return base;
+}
+
+// Tokens of one work-group: 16 while many work-groups are quicker than few with
+// more rounds (1024 tokens of 256 experts: 13.6 us against 24), 64 beyond, as
+// the second launch reads all rows of counts in every work-group (16384 tokens of
+// 128 experts: 17.3 us against 21.9 with rows of 16 tokens).
+int block_tokens(int64_t tokens) { return tokens <= ROUTE_WAVES ? 16 : 64; }
+
+// A work-group takes `block` tokens, blockDim / L of them at a time (ONE: it is
+// the only one).  Ranks within an expert come from a mask per expert with a bit
+// for each token: a token names an expert at most once.
+template <int L, int PER, Mode MODE, bool ONE>
+__global__ void __launch_bounds__(1024) route_kernel(RouteArgs a, int block) {
+    extern __shared__ uint64_t mask[];  // [experts]; ONE: ids and weights of the pairs, offsets
+    __shared__ int part[16];
+    const int tid = threadIdx.x, threads = blockDim.x, lane = tid % L;
     int* const lds_id = reinterpret_cast<int*>(mask + a.experts);
-    float* const lds_w = reinterpret_cast<float*>(lds_id + ROUTE_BLOCK * a.top_k);
-    const int64_t first = (int64_t)blockIdx.x * ROUTE_BLOCK;
-    const int here = (int)(a.tokens - first < ROUTE_BLOCK ? a.tokens - first : ROUTE_BLOCK);
-    for (int e = tid; e < a.experts; e += T) mask[e] = 0;
+    float* const lds_w = reinterpret_cast<float*>(lds_id + block * a.top_k);
+    const int64_t first = (int64_t)blockIdx.x * block;
+    const int here = (int)(a.tokens - first < block ? a.tokens - first : block);
+    for (int e = tid; e < a.experts; e += threads) mask[e] = 0;
     __syncthreads();
-    for (int t = slot; t < ROUTE_BLOCK; t += TOKENS) {
-        if (t - slot >= here) break;  // the same for all
-        const bool live = t < here;
-        const int64_t token = first + (live ? t : 0);
-        Chosen c = choose<L, PER, BIAS>(a, token, lane);
-        if (!live || lane >= a.top_k) continue;
-        if (a.keep && !a.keep[token]) c = Chosen{-1, 0.f};
-        const int64_t pair = token * a.top_k + lane;
-        if (a.ids) a.ids[pair] = c.id;
-        if (a.weights) a.weights[pair] = c.w;
-        lds_id[t * a.top_k + lane] = c.id;
-        lds_w[t * a.top_k + lane] = c.w;
-        if (c.id >= 0) atomicOr(reinterpret_cast<unsigned long long*>(mask + c.id), 1ull << t);
+    for (int t0 = 0; t0 < here; t0 += threads / L) {
+        const int t = t0 + tid / L;
+        const int64_t token = first + (t < here ? t : 0);
+        Chosen c = choose<L, PER, MODE>(a, token, lane);
+        if (t < here && lane < a.top_k) {
+            if (a.keep && !a.keep[token]) c = Chosen{-1, 0.f};
+            const int64_t pair = token * a.top_k + lane;
+            a.ids[pair] = c.id;
+            a.weights[pair] = c.w;
+            if (ONE) {
+                lds_id[t * a.top_k + lane] = c.id;
+                lds_w[t * a.top_k + lane] = c.w;
+            }
+            if (c.id >= 0) atomicOr(reinterpret_cast<unsigned long long*>(mask + c.id), 1ull << t);
+        }
     }
     if (!a.offsets) return;
     __syncthreads();
-    const int pairs = here * a.top_k;
     if constexpr (ONE) {
-        // Offsets: sums over the experts before, T of them at a time; the
-        // masks' places take the offsets.
-        int base = 0;
-        int* const off = reinterpret_cast<int*>(lds_w + ROUTE_BLOCK * a.top_k);
-        for (int e0 = 0; e0 < a.experts; e0 += T) {
-            const int e = e0 + tid;
-            const int n = e < a.experts ? __popcll(mask[e]) : 0;
-            int sum = n;
-            for (int d = 1; d < 64; d *= 2) {
-                const int before = __shfl_up(sum, d, 64);
-                if ((tid & 63) >= d) sum += before;
-            }
-            if ((tid & 63) == 63) part[tid >> 6] = sum;
-            __syncthreads();
-            int before = base;
-            for (int i = 0; i < T / 64; ++i) {
-                if (i < tid >> 6) before += part[i];
-                base += part[i];
-            }
-            if (e < a.experts) {
-                off[e] = before + sum - n;
-                a.offsets[e] = before + sum - n;
-            }
-            __syncthreads();
-        }
-        if (tid == 0) a.offsets[a.experts] = base;
-        for (int p = tid; p < pairs; p += T) {
+        int* const off = reinterpret_cast<int*>(lds_w + block * a.top_k);
+        const int all = sums_before(a.experts, part, [&](int e) { return (int)__popcll(mask[e]); },
+                                    [&](int e, int before, int) {
+                                        off[e] = before;
+                                        a.offsets[e] = before;
+                                    });
+        if (tid == 0) a.offsets[a.experts] = all;
+        for (int p = tid; p < here * a.top_k; p += threads) {
             const int e = lds_id[p], t = p / a.top_k;
-            const int row = e < 0 ? -1 : off[e] + __popcll(mask[e] & ((1ull << t) - 1));
+            const int row = e < 0 ? -1 : off[e] + (int)__popcll(mask[e] & ((1ull << t) - 1));
             if (a.pair_row) a.pair_row[p] = row;
             if (row < 0) continue;
             if (a.pair_token) a.pair_token[row] = t;
             if (a.pair_weight) a.pair_weight[row] = lds_w[p];
         }
     } else {
-        const int width = (a.experts + 7) & ~7;
-        uint16_t* const counts = a.counts + (int64_t)blockIdx.x * width;
-        for (int e = tid; e < width; e += T) counts[e] = e < a.experts ? (uint16_t)__popcll(mask[e]) : (uint16_t)0;
+        const int width = (a.experts + 15) & ~15;
+        uint8_t* const counts = a.counts + (int64_t)blockIdx.x * width;
+        for (int e = 4 * tid; e < width; e += 4 * threads) {
+            u32 n = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (e + j < a.experts) n |= (u32)__popcll(mask[e + j]) << (8 * j);
+            *reinterpret_cast<u32*>(counts + e) = n;
+        }
     }
 }
 
-// Second launch where several work-groups routed: each takes the tokens of one
-// of them again, adds up what the experts got before, and places its pairs.
-template <int T>
-__global__ void __launch_bounds__(T) route_place_kernel(RouteArgs a, int blocks) {
-    extern __shared__ uint64_t mask[];  // [experts], then [2][experts]: rows before this work-group, all rows
-    __shared__ int part[T / 64];
-    const int tid = threadIdx.x;
+// Sums of CHUNK rows of counts, for every expert: 16 experts a thread, rows of
+// them side by side.
+__global__ void __launch_bounds__(256) route_sums_kernel(const uint8_t* counts, u32* sums, int width, int blocks) {
+    extern __shared__ u32 all_of[];  // [width]
+    const int tid = threadIdx.x, pieces = width / 16, side = 256 / pieces;
+    const int row0 = (int)blockIdx.x * CHUNK, rows = blocks - row0 < CHUNK ? blocks - row0 : CHUNK;
+    for (int e = tid; e < width; e += 256) all_of[e] = 0;
+    __syncthreads();
+    if (tid / pieces < side) {
+        const int piece = tid % pieces;
+        const u32x4* const p = reinterpret_cast<const u32x4*>(counts) + (int64_t)row0 * pieces + piece;
+        for (int b = tid / pieces; b < rows; b += side) {
+            const u32x4 v = p[(int64_t)b * pieces];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const u32 n = v[j / 4] >> (8 * (j % 4)) & 255u;
+                if (n) atomicAdd(all_of + 16 * piece + j, n);
+            }
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < width; e += 256) sums[(int64_t)blockIdx.x * width + e] = all_of[e];
+}
+
+// Last launch where several work-groups routed: each takes 64 tokens, adds up
+// what the experts got before, and places its pairs.  Counts (`blocks` rows, of
+// `block` tokens each) are read 16 experts a thread, rows of them side by side;
+// where there are sums of CHUNK rows, those and the rows of the own chunk.
+constexpr int PLACE = 64;
+__global__ void __launch_bounds__(256) route_place_kernel(RouteArgs a, int block, int blocks, const u32* sums) {
+    extern __shared__ uint64_t mask[];  // [experts], then [2][width]: rows before this work-group, all rows
+    __shared__ int part[4];
+    const int tid = threadIdx.x, width = (a.experts + 15) & ~15, mine = blockIdx.x * (PLACE / block);
     int* const before = reinterpret_cast<int*>(mask + a.experts);
-    const int width = (a.experts + 7) & ~7;
-    const int64_t first = (int64_t)blockIdx.x * ROUTE_BLOCK;
-    const int here = (int)(a.tokens - first < ROUTE_BLOCK ? a.tokens - first : ROUTE_BLOCK);
+    int* const all = before + width;
+    const int64_t first = (int64_t)blockIdx.x * PLACE;
+    const int here = (int)(a.tokens - first < PLACE ? a.tokens - first : PLACE);
     const int pairs = here * a.top_k;
-    for (int e = tid; e < a.experts; e += T) mask[e] = 0;
+    for (int e = tid; e < a.experts; e += 256) mask[e] = 0;
+    for (int e = tid; e < 2 * width; e += 256) before[e] = 0;
     __syncthreads();
     const int32_t* const ids = a.ids + first * a.top_k;
-    for (int p = tid; p < pairs; p += T) {
+    for (int p = tid; p < pairs; p += 256) {
         const int e = ids[p];
         if (e >= 0) atomicOr(reinterpret_cast<unsigned long long*>(mask + e), 1ull << (p / a.top_k));
     }
-    int base = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += T) {
-        const int e = e0 + tid;
-        int mine = 0, all = 0;
-        if (e < a.experts) {
-            for (int b = 0; b < blocks; ++b) {
-                const int n = a.counts[(int64_t)b * width + e];
-                all += n;
-                if (b < (int)blockIdx.x) mine += n;
-            }
+    int from = 0, to = blocks;
+    if (sums) {
+        const int own = mine / CHUNK, chunks = (blocks + CHUNK - 1) / CHUNK;
+        from = own * CHUNK;
+        to = from + CHUNK < blocks ? from + CHUNK : blocks;
+        for (int i = tid; i < chunks * width; i += 256) {
+            const int c = i / width, e = i % width, n = (int)sums[i];
+            if (n == 0 || c == own) continue;
+            atomicAdd(all + e, n);
+            if (c < own) atomicAdd(before + e, n);
         }
-        int sum = all;
-        for (int d = 1; d < 64; d *= 2) {
-            const int x = __shfl_up(sum, d, 64);
-            if ((tid & 63) >= d) sum += x;
-        }
-        if ((tid & 63) == 63) part[tid >> 6] = sum;
-        __syncthreads();
-        int at = base;
-        for (int i = 0; i < T / 64; ++i) {
-            if (i < tid >> 6) at += part[i];
-            base += part[i];
-        }
-        at += sum - all;
-        if (e < a.experts) {
-            before[e] = at + mine;
-            if (blockIdx.x == 0) a.offsets[e] = at;
-        }
-        __syncthreads();
     }
-    if (blockIdx.x == 0 && tid == 0) a.offsets[a.experts] = base;
-    for (int p = tid; p < pairs; p += T) {
+    const int pieces = width / 16, side = 256 / pieces;  // 1 to 64 pieces of a row, so 4 rows at a time at least
+    const int piece = tid % pieces, row0 = tid / pieces;
+    if (row0 < side) {
+        // Sums of bytes, two in a register (of at most 64 each, so 1023 rows before they are added up).
+        int rows = 0;
+        u32 sum[8], low[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = low[j] = 0;
+        const auto hand_in = [&] {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int e = 16 * piece + 4 * (j / 2) + j % 2;
+                if (low[j] & 0xffff) atomicAdd(before + e, (int)(low[j] & 0xffff));
+                if (low[j] >> 16) atomicAdd(before + e + 2, (int)(low[j] >> 16));
+                if (sum[j] & 0xffff) atomicAdd(all + e, (int)(sum[j] & 0xffff));
+                if (sum[j] >> 16) atomicAdd(all + e + 2, (int)(sum[j] >> 16));
+                sum[j] = low[j] = 0;
+            }
+            rows = 0;
+        };
+        const auto add = [&](u32x4 v, bool earlier) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const u32 n = v[j / 2] >> (8 * (j % 2)) & 0x00ff00ffu;  // bytes j % 2 and j % 2 + 2
+                sum[j] += n;
+                low[j] += earlier ? n : 0;
+            }
+        };
+        const u32x4* const counts = reinterpret_cast<const u32x4*>(a.counts) + piece;
+        int b = from + row0;
+        for (; b + 3 * side < to; b += 4 * side) {
+            u32x4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = counts[(int64_t)(b + i * side) * pieces];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) add(v[i], b + i * side < mine);
+            if ((rows += 4) > 1000) hand_in();
+        }
+        for (; b < to; b += side) add(counts[(int64_t)b * pieces], b < mine);
+        hand_in();
+    }
+    __syncthreads();
+    const int rows = sums_before(a.experts, part, [&](int e) { return all[e]; },
+                                 [&](int e, int at, int) {
+                                     before[e] += at;
+                                     if (blockIdx.x == 0) a.offsets[e] = at;
+                                 });
+    if (blockIdx.x == 0 && tid == 0) a.offsets[a.experts] = rows;
+    for (int p = tid; p < pairs; p += 256) {
         const int e = ids[p], t = p / a.top_k;
-        const int row = e < 0 ? -1 : before[e] + __popcll(mask[e] & ((1ull << t) - 1));
+        const int row = e < 0 ? -1 : before[e] + (int)__popcll(mask[e] & ((1ull << t) - 1));
         const int64_t pair = first * a.top_k + p;
         if (a.pair_row) a.pair_row[pair] = row;
         if (row < 0) continue;
@@ -403,45 +687,66 @@ __global__ void __launch_bounds__(T) route_place_kernel(RouteArgs a, int blocks)
     }
 }
 
-template <int T, int L, int PER, bool BIAS>
+int64_t count_bytes(int64_t blocks, int experts) { return blocks * ((experts + 15) & ~15); }
+
+template <int L, int PER, Mode MODE>
 hipError_t launch(const RouteArgs& a, hipStream_t st) {
-    const size_t lds = (size_t)a.experts * 12 + (size_t)ROUTE_BLOCK * a.top_k * 8;
-    const int64_t blocks = (a.tokens + ROUTE_BLOCK - 1) / ROUTE_BLOCK;
-    if (route_in_one(a.tokens)) {
-        route_kernel<T, L, PER, BIAS, true><<<dim3(1), dim3(T), lds, st>>>(a);
+    constexpr int AT_ONCE = 1024 / L;
+    if (a.tokens <= AT_ONCE) {
+        const int threads = a.tokens * L < 64 ? 64 : (int)((a.tokens * L + 63) / 64 * 64);
+        const size_t lds = (size_t)a.experts * 12 + (size_t)AT_ONCE * a.top_k * 8;
+        route_kernel<L, PER, MODE, true><<<dim3(1), dim3(threads), lds, st>>>(a, AT_ONCE);
         return hipGetLastError();
     }
-    route_kernel<T, L, PER, BIAS, false><<<dim3((unsigned)blocks), dim3(T), lds, st>>>(a);
+    const int block = block_tokens(a.tokens);
+    const int64_t blocks = (a.tokens + block - 1) / block;
+    route_kernel<L, PER, MODE, false><<<dim3((unsigned)blocks), dim3(block * L < 1024 ? block * L : 1024), (size_t)a.experts * 8, st>>>(a, block);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.offsets) return e;
-    route_place_kernel<256><<<dim3((unsigned)blocks), dim3(256), (size_t)a.experts * 12, st>>>(a, (int)blocks);
+    const int width = (a.experts + 15) & ~15;
+    u32* sums = nullptr;
+    if (blocks > CHUNKED) {
+        sums = reinterpret_cast<u32*>(a.counts + count_bytes(blocks, a.experts));
+        route_sums_kernel<<<dim3((unsigned)((blocks + CHUNK - 1) / CHUNK)), dim3(256), (size_t)width * 4, st>>>(a.counts, sums, width, (int)blocks);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    const size_t place = (size_t)a.experts * 8 + (size_t)width * 8;
+    route_place_kernel<<<dim3((unsigned)((a.tokens + PLACE - 1) / PLACE)), dim3(256), place, st>>>(a, block, (int)blocks, sums);
     return hipGetLastError();
 }
 
-template <int T, int L, int PER>
-hipError_t launch_bias(const RouteArgs& a, hipStream_t st) {
-    return a.bias ? launch<T, L, PER, true>(a, st) : launch<T, L, PER, false>(a, st);
+template <int L, int PER>
+hipError_t launch_mode(const RouteArgs& a, hipStream_t st) {
+    if (a.bias) return launch<L, PER, BIASED>(a, st);
+    if (a.groups > 1 && a.group_best == 2) return launch<L, PER, PAIRS>(a, st);
+    return launch<L, PER, LOGITS>(a, st);
 }
 
 }  // namespace
 
-bool route_in_one(int64_t tokens) { return tokens <= ROUTE_BLOCK; }
-
 size_t route_workspace(int64_t tokens, int experts) {
-    if (route_in_one(tokens)) return 0;
-    return (size_t)((tokens + ROUTE_BLOCK - 1) / ROUTE_BLOCK) * (size_t)((experts + 7) & ~7) * 2;
+    if (tokens <= ROUTE_ONE) return 0;
+    const int block = block_tokens(tokens);
+    const int64_t blocks = (tokens + block - 1) / block;
+    return (size_t)(count_bytes(blocks, experts) + (blocks > CHUNKED ? 4 * count_bytes((blocks + CHUNK - 1) / CHUNK, experts) : 0));
 }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
-    if (a.top_k <= 16 && a.groups <= 16) {
-        if (a.experts <= 64) return launch_bias<256, 16, 4>(a, st);
-        if (a.experts <= 128) return launch_bias<256, 16, 8>(a, st);
-        if (a.experts <= 256) return launch_bias<256, 16, 16>(a, st);
+    // A wave for each token is the shortest way through (one token of 128
+    // experts: 4.5 us against 6.3 with 16 lanes); four tokens to a wave take
+    // fewer instructions in all and are quicker once the device is full (16384
+    // tokens of 128 experts, ids only: 9.3 us against 13.7), and where they save
+    // the second launch (37 tokens: 8.4 us against 10.4).
+    const bool one = a.tokens > ROUTE_ONE && a.tokens <= ROUTE_ONE_16 && !a.bias && a.groups == 1;
+    if ((a.tokens > ROUTE_WAVES || one) && a.top_k <= 16 && a.groups <= 16) {
+        if (a.experts <= 64) return launch_mode<16, 4>(a, st);
+        if (a.experts <= 128) return launch_mode<16, 8>(a, st);
     }
-    if (a.experts <= 128) return launch_bias<256, 64, 2>(a, st);
-    if (a.experts <= 256) return launch_bias<256, 64, 4>(a, st);
-    if (a.experts <= 512) return launch_bias<256, 64, 8>(a, st);
-    return launch_bias<256, 64, 16>(a, st);
+    if (a.experts <= 64) return launch_mode<64, 1>(a, st);
+    if (a.experts <= 128) return launch_mode<64, 2>(a, st);
+    if (a.experts <= 256) return launch_mode<64, 4>(a, st);
+    if (a.experts <= 512) return launch_mode<64, 8>(a, st);
+    return launch_mode<64, 16>(a, st);
 }
 
 }  // namespace qmm

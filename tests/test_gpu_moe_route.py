@@ -204,7 +204,7 @@ def test_without_groups_and_without_tokens():
     assert (out["offsets"] == UNTOUCHED).all()
 
 
-@pytest.mark.parametrize("tokens,experts", [(5000, 128), (4097, 384), (9001, 8)])
+@pytest.mark.parametrize("tokens,experts", [(5000, 128), (4096, 100), (4097, 384), (9001, 8), (16384, 40), (16385, 129), (70001, 20), (262145, 16)])
 def test_many_tokens(tokens, experts):
     # Against the oracle for a sample's choices, and the grouping whole.
     rng = np.random.default_rng(tokens)
