@@ -173,6 +173,7 @@ qmm_status qmm_quantize_rows(const void* x, int x_fp16, int64_t x_stride, int8_t
     a.k = (int)k;
     a.f16 = x_fp16 != 0;
     a.vec = a.stride % 4 == 0 && aligned(x, 4 * size);
+    a.vec8 = a.stride % 8 == 0 && aligned(x, 16);
     int cus = 0;
     qmm_status st = current_cus(&cus);
     if (st != QMM_OK) return st;
@@ -225,7 +226,7 @@ qmm_status qmm_moe_gather(const void* rows, int rows_fp16, const int32_t* pair_r
     a.n = n;
     a.top_k = top_k;
     a.f16 = rows_fp16 != 0;
-    a.vec = n % 4 == 0 && aligned(rows, rows_fp16 ? 8 : 16) && aligned(residual, 16) && aligned(y, 16);
+    a.vec = n % (rows_fp16 ? 8 : 4) == 0 && aligned(rows, 16) && aligned(residual, 16) && aligned(y, 16);
     int cus = 0;
     qmm_status st = current_cus(&cus);
     if (st != QMM_OK) return st;

@@ -2,67 +2,74 @@
 //   y[t] = residual[t] + sum_j weights[t][j] * rows[pair_row[t][j]],
 // summed in the order of j in fp32, so results repeat bit for bit.
 //
-// Bound by memory: every row is read once, y written once.
+// Bound by memory: every row is read once, y written once.  A thread owns 16
+// bytes of a row (one load); indices and weights are the same for a whole
+// work-group, and the rows of up to eight choices are asked for before the first
+// is added.
 #include "layer_device.h"
 #include "moe_kernels.h"
 
 namespace qmm {
 namespace {
 
-typedef f16 f16x4v __attribute__((ext_vector_type(4)));
-
 // A thread owns V neighbouring columns of one token.
 template <int V, typename F>
 __global__ void __launch_bounds__(256) gather_kernel(GatherArgs a) {
     typedef F vec __attribute__((ext_vector_type(V)));
-    typedef float fvec __attribute__((ext_vector_type(V)));
+    constexpr int AHEAD = 8;
     const int64_t t = blockIdx.x;
     const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * V;
     if (c >= a.n) return;
+    const int32_t* const at = a.pair_row + t * a.top_k;
+    const float* const w = a.weights + t * a.top_k;
+    const F* const rows = static_cast<const F*>(a.rows) + c;
     float sum[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) sum[i] = 0.f;
-    for (int j = 0; j < a.top_k; ++j) {
-        const int64_t row = a.pair_row[t * a.top_k + j];
-        if (row < 0 || row >= a.p_rows) continue;
-        const float w = a.weights[t * a.top_k + j];
-        const F* p = static_cast<const F*>(a.rows) + row * a.n + c;
-        if constexpr (V > 1) {
-            const vec v = *reinterpret_cast<const vec*>(p);
+    for (int j0 = 0; j0 < a.top_k; j0 += AHEAD) {
+        vec v[AHEAD];
+        bool there[AHEAD];
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] = fmaf(w, (float)v[i], sum[i]);
-        } else {
-            sum[0] = fmaf(w, (float)p[0], sum[0]);
+        for (int j = 0; j < AHEAD; ++j) {
+            const int64_t row = j0 + j < a.top_k ? at[j0 + j] : -1;
+            there[j] = row >= 0 && row < a.p_rows;
+            if (there[j]) v[j] = *reinterpret_cast<const vec*>(rows + row * a.n);
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (!there[j]) continue;
+            const float f = w[j0 + j];
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] = fmaf(f, (float)v[j][i], sum[i]);
         }
     }
-    if (a.residual) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] += a.residual[t * a.n + c + i];
-    }
-    if constexpr (V > 1) {
-        fvec v;
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = sum[i];
-        *reinterpret_cast<fvec*>(a.y + t * a.n + c) = v;
+    float* const y = a.y + t * a.n + c;
+    if constexpr (V == 1) {
+        y[0] = a.residual ? a.residual[t * a.n + c] + sum[0] : sum[0];
     } else {
-        a.y[t * a.n + c] = sum[0];
+        f32x4 out[V / 4];
+#pragma unroll
+        for (int i = 0; i < V; ++i) out[i / 4][i % 4] = sum[i];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            if (a.residual) out[i] += reinterpret_cast<const f32x4*>(a.residual + t * a.n + c)[i];
+            reinterpret_cast<f32x4*>(y)[i] = out[i];
+        }
     }
+}
+
+template <int V, typename F>
+hipError_t launch(const GatherArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)a.tokens, (unsigned)((a.n + 256 * V - 1) / (256 * V)));
+    gather_kernel<V, F><<<grid, dim3(256), 0, st>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_gather(const GatherArgs& a, hipStream_t st) {
-    const unsigned width = a.vec ? 1024 : 256;
-    const dim3 grid((unsigned)a.tokens, (unsigned)((a.n + width - 1) / width));
-    if (a.vec && a.f16)
-        gather_kernel<4, f16><<<grid, 256, 0, st>>>(a);
-    else if (a.vec)
-        gather_kernel<4, float><<<grid, 256, 0, st>>>(a);
-    else if (a.f16)
-        gather_kernel<1, f16><<<grid, 256, 0, st>>>(a);
-    else
-        gather_kernel<1, float><<<grid, 256, 0, st>>>(a);
-    return hipGetLastError();
+    if (a.f16) return a.vec ? launch<8, f16>(a, st) : launch<1, f16>(a, st);
+    return a.vec ? launch<4, float>(a, st) : launch<1, float>(a, st);
 }
 
 }  // namespace qmm

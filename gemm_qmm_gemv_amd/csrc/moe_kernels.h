@@ -38,7 +38,7 @@ struct QuantizeArgs {
     float* scales;
     int64_t stride, rows;
     int k;
-    bool f16, vec;
+    bool f16, vec, vec8;  // rows in runs of four values, of eight
 };
 hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t st);
 

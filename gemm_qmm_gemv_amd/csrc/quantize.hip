@@ -1,12 +1,13 @@
 // quantize.hip -- rows of activations to 8-bit codes with a scale for each row:
 //   scale = fp32(max |x| / 127),  code = round(x / scale), ties to even.
 //
-// Bound by memory.  A work-group holds one row in registers (PER runs of four
-// per thread), so that the maximum and the codes cost one read.  The quotient
-// is formed by a product with 1 / scale and put right by what it leaves over:
-// x - code * scale is exact in one fused step (the code's product with the scale
-// and x agree in all leading bits), so the code is the whole number next to
-// the real quotient, at less than a division's cost.
+// Bound by memory, and nearly as much by the vector units: what a value costs
+// there is kept to a handful of instructions.  The whole number next to x / scale
+// comes out of one fused step with 1.5 * 2^23 (its low bits are the code, two's
+// complement), and what it leaves over, x - code * scale, is exact in another: the
+// code is the right one if that is less than half a scale.  Where it is not
+// (the inverse is rounded, so next to a border it may not be), and on it, the
+// codes are worked out again with the border looked at.
 #include "layer_device.h"
 #include "moe_kernels.h"
 
@@ -23,6 +24,60 @@ __device__ __forceinline__ int code_of(float x, float scale, float inv) {
     if (left > half || (left == half && odd)) q += 1.f;
     if (left < -half || (left == -half && odd)) q -= 1.f;
     return (int)fminf(fmaxf(q, -127.f), 127.f);
+}
+
+// A row's scale from its largest magnitude, and what its codes are made with.
+struct Unit {
+    float scale, up, s, inv;
+};
+__device__ __forceinline__ Unit unit_of(float top) {
+    Unit u;
+    const bool finite = top < __builtin_huge_valf();
+    u.scale = finite ? top / 127.f : __builtin_nanf("");
+    // 1 / scale may leave fp32 for the smallest scales: such rows are scaled up
+    // first, which is exact.
+    u.up = u.scale < 0x1p-100f ? 0x1p100f : 1.f;
+    u.s = u.scale * u.up;
+    u.inv = finite && u.s > 0.f ? 1.f / u.s : 0.f;
+    return u;
+}
+// Largest magnitude so far, as its bits: a NaN's are above an infinity's, that are
+// above all others.
+__device__ __forceinline__ void larger(u32& top, float v) {
+    const u32 b = __builtin_bit_cast(u32, v) & 0x7fffffffu;
+    top = b > top ? b : top;
+}
+__device__ __forceinline__ float max_f32(float a, float b) { return fmaxf(a, b); }
+// Over a wave; infinite if any value is not finite.
+__device__ __forceinline__ float top_of(u32 top) {
+    if (top > 0x7f800000u) top = 0x7f800000u;
+    return over_lanes<64>(__builtin_bit_cast(float, top), max_f32);
+}
+
+__device__ __forceinline__ u32 four_codes_checked(float a, float b, float c, float d, float up, float s, float inv) {
+    const float v[4] = {a, b, c, d};
+    u32 w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int q = inv > 0.f ? code_of(v[j] * up, s, inv) : 0;
+        w |= ((u32)q & 255u) << (8 * j);
+    }
+    return w;
+}
+__device__ __forceinline__ u32 four_codes(const float* v, const Unit& u) {
+    u32 r[4];
+    float off = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float m = fmaf(v[j], u.inv, 12582912.f);  // rounds to a whole number
+        r[j] = __builtin_bit_cast(u32, m);
+        off = fmaxf(off, fabsf(fmaf(12582912.f - m, u.s, v[j])));
+    }
+    // (Rows of zeros, of tiny and of values that are not finite come here, too.)
+    if (__any(!(off < 0.5f * u.s) || u.up != 1.f))
+        return four_codes_checked(v[0], v[1], v[2], v[3], u.up, u.s, u.inv);
+    const u32 lo = __builtin_amdgcn_perm(r[1], r[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(r[3], r[2], 0x04000c0cu);
+    return lo | hi;
 }
 
 template <int T, int PER, bool VEC>
@@ -59,45 +114,72 @@ __global__ void __launch_bounds__(T) quantize_kernel(QuantizeArgs a) {
             }
         }
     }
-    // A value that is not finite makes the row's scale NaN (x - x is NaN then,
-    // and the sum of zeros elsewhere).
-    float top = 0.f, bad = 0.f;
+    // A value that is not finite makes the row's scale NaN.
+    u32 bits = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            top = fmaxf(top, fabsf(v[i][j]));
-            bad += v[i][j] - v[i][j];
-        }
-    if (bad != bad) top = __builtin_huge_valf();
-    const auto larger = [](float x, float y) { return fmaxf(x, y); };
-    top = over_lanes<64>(top, larger);
+        for (int j = 0; j < 4; ++j) larger(bits, v[i][j]);
+    float top = top_of(bits);
     if constexpr (T > 64) {
         if ((tid & 63) == 0) lds[tid >> 6] = top;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < T / 64; ++i) top = fmaxf(top, lds[i]);
     }
-    const bool finite = top < __builtin_huge_valf();
-    const float scale = finite ? top / 127.f : __builtin_nanf("");
-    // 1 / scale may leave fp32 for the smallest scales: such rows are scaled up
-    // first, which is exact.
-    const float up = scale < 0x1p-100f ? 0x1p100f : 1.f;
-    const float s = scale * up, inv = finite && s > 0.f ? 1.f / s : 0.f;
+    const Unit u = unit_of(top);
     int8_t* const out = a.codes + row * (int64_t)a.k;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = (i * T + tid) * 4;
         if (e >= a.k) continue;
-        u32 w = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int q = inv > 0.f ? code_of(v[i][j] * up, s, inv) : 0;
-            w |= ((u32)q & 255u) << (8 * j);
-        }
-        *reinterpret_cast<u32*>(out + e) = w;
+        *reinterpret_cast<u32*>(out + e) = four_codes(v[i], u);
     }
-    if (tid == 0) a.scales[row] = scale;
+    if (tid == 0) a.scales[row] = u.scale;
+}
+
+// Many rows: a wave for each, N runs of eight values a lane (16 bytes of fp16,
+// one store of codes), no meeting of waves.
+template <int N, bool F16>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(QuantizeArgs a) {
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= a.rows) return;
+    const int lane = threadIdx.x & 63;
+    float v[N][8];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = (i * 64 + lane) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        if (e >= a.k) continue;
+        if constexpr (F16) {
+            const f16x8 w = *reinterpret_cast<const f16x8*>(static_cast<const f16*>(a.x) + row * a.stride + e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = (float)w[j];
+        } else {
+            const f32x4* const p = reinterpret_cast<const f32x4*>(static_cast<const float*>(a.x) + row * a.stride + e);
+            const f32x4 x = p[0], y = p[1];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[i][j] = x[j];
+                v[i][j + 4] = y[j];
+            }
+        }
+    }
+    u32 bits = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) larger(bits, v[i][j]);
+    const Unit u = unit_of(top_of(bits));
+    int8_t* const out = a.codes + row * (int64_t)a.k;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = (i * 64 + lane) * 8;
+        if (e >= a.k) continue;
+        *reinterpret_cast<u32x2*>(out + e) = u32x2{four_codes(v[i], u), four_codes(v[i] + 4, u)};
+    }
+    if (lane == 0) a.scales[row] = u.scale;
 }
 
 template <int T, int PER>
@@ -109,9 +191,24 @@ hipError_t launch(const QuantizeArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <int N>
+hipError_t launch_rows(const QuantizeArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)((a.rows + 3) / 4));
+    if (a.f16)
+        quantize_rows_kernel<N, true><<<grid, dim3(256), 0, st>>>(a);
+    else
+        quantize_rows_kernel<N, false><<<grid, dim3(256), 0, st>>>(a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t st) {
+    // A wave for each row, where a work-group has little to do for one and there are
+    // rows for all waves (32768 rows of 768 in fp16: 17.8 us against 26.7); longer
+    // rows take the same either way (8192 of 2048: 14.6 against 13.9), and few are
+    // quicker through with four waves each (37 of 2048: 4.5 against 2.8).
+    if (a.vec8 && a.k <= 1024 && a.rows >= 2048) return a.k <= 512 ? launch_rows<1>(a, st) : launch_rows<2>(a, st);
     if (a.k <= 1024) return launch<256, 1>(a, st);
     if (a.k <= 2048) return launch<256, 2>(a, st);
     if (a.k <= 4096) return launch<256, 4>(a, st);
