@@ -7,6 +7,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import typing
 
 import numpy as np
 import torch
@@ -15,7 +16,9 @@ from . import (QMM_OK, GemvDesc, KvCache, _check, _stream, load, qmm_attn_cache,
                qmm_attn_prompt, qmm_gemm, qmm_gemm_f16out, qmm_gemm_workspace_bytes, qmm_gemv, qmm_gemv_batch_prepare,
                qmm_gemv_swiglu, qmm_moe_swiglu, qmm_gemv_residual, qmm_moe_combine, qmm_gemm_grouped,
                qmm_gemm_grouped_workspace_bytes,
-               qmm_gemv_batched, qmm_kv_append, qmm_moe_gemm, qmm_norm_residual, qmm_unpack)
+               qmm_gemv_batched, qmm_kv_append, qmm_moe_gemm, qmm_norm_residual, qmm_unpack, qmm_moe_route,
+               qmm_moe_route_workspace_bytes, qmm_quantize_rows, qmm_gemm_i8, qmm_moe_gemm_i8, qmm_moe_swiglu_i8,
+               qmm_moe_gather)
 
 
 def device_tensor(a: np.ndarray, device="cuda") -> torch.Tensor:
@@ -140,6 +143,147 @@ def unpack(dq: dict, stream=None) -> torch.Tensor:
     codes = torch.empty((dq["n"], dq["k"]), dtype=torch.uint8, device=dq["w"].device)
     qmm_unpack(dq["w"], codes, dq["n"], dq["k"], dq["bits"], stream=stream)
     return codes
+
+
+class Routing(typing.NamedTuple):
+    """What moe_route gives: experts and weights [tokens, top_k] of each token, and, if grouped, what the experts'
+    products and moe_gather take: row of each pair, offsets [experts + 1], token and weight of each row."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    pair_row: torch.Tensor | None
+    offsets: torch.Tensor | None
+    pair_token: torch.Tensor | None
+    pair_weight: torch.Tensor | None
+
+
+def route_workspace(tokens: int, experts: int, top_k: int, device="cuda") -> torch.Tensor:
+    """Scratch for moe_route calls of this size, one after another on one stream."""
+    return torch.empty(max(16, qmm_moe_route_workspace_bytes(tokens, experts, top_k)), dtype=torch.uint8, device=device)
+
+
+def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None, sigmoid: bool = False, groups: int = 1,
+              top_groups: int = 1, group_best: int = 1, renormalize: bool = True, scale: float = 1.0,
+              keep: torch.Tensor | None = None, grouped: bool = True, workspace: torch.Tensor | None = None,
+              stream=None) -> Routing:
+    """Experts of each token from the router's logits [tokens, experts] (fp32 or fp16; a column range of a wider tensor
+    will do); keep [tokens] bool or uint8: tokens of 0 are padding.  Behind the last row pair_token and pair_weight hold
+    anything."""
+    _on_device(logits, bias, keep, workspace)
+    tokens, experts = logits.shape
+    _floating("logits", logits)
+    _dense("bias", bias, torch.float32, experts)
+    if keep is not None and keep.dtype == torch.bool:
+        keep = keep.view(torch.uint8)
+    _vector("keep", keep, torch.uint8, tokens)
+    pairs, like = (tokens, top_k), logits.device
+    ids, weights = _output(pairs, torch.int32, like, stream), _output(pairs, torch.float32, like, stream)
+    rest = (None,) * 4
+    if grouped:
+        rest = (_output(pairs, torch.int32, like, stream), _output((experts + 1,), torch.int32, like, stream),
+                _output((tokens * top_k,), torch.int32, like, stream), _output((tokens * top_k,), torch.float32, like, stream))
+        if workspace is None:
+            # Made and given back on the current stream.
+            assert stream is None, "a call on another stream needs a workspace of its own"
+            workspace = route_workspace(tokens, experts, top_k, like)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace is not dense")
+    out = Routing(ids, weights, *rest)
+    qmm_moe_route(logits, logits.dtype == torch.float16, _rows(logits), bias, sigmoid, groups, top_groups, group_best, top_k,
+                  renormalize, scale, keep, out.ids, out.weights, out.pair_row, out.offsets, out.pair_token, out.pair_weight,
+                  workspace, 0 if workspace is None else workspace.numel() * workspace.element_size(), tokens, experts,
+                  stream=stream)
+    return out
+
+
+def moe_gather(rows: torch.Tensor, pair_row: torch.Tensor, weights: torch.Tensor, residual: torch.Tensor | None = None,
+               y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[t] = residual[t] + sum_j weights[t, j] * rows[pair_row[t, j]] (rows [p, n] fp32 or fp16; residual may be y)."""
+    _on_device(rows, pair_row, weights, residual, y)
+    p, n = rows.shape
+    tokens, top_k = pair_row.shape
+    _floating("rows", rows)
+    _dense("rows", rows, rows.dtype, p, n)
+    _dense("pair_row", pair_row, torch.int32, tokens, top_k)
+    _dense("weights", weights, torch.float32, tokens, top_k)
+    _dense("residual", residual, torch.float32, tokens, n)
+    _dense("y", y, torch.float32, tokens, n)
+    if y is None:
+        y = _output((tokens, n), torch.float32, rows.device, stream)
+    qmm_moe_gather(rows, rows.dtype == torch.float16, pair_row, weights, residual, y, tokens, top_k, p, n, stream=stream)
+    return y
+
+
+def quantize_rows(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """(codes int8 [rows, k], scales fp32 [rows]): x = scale * code, scale = max |x| / 127 of each row (x fp32 or fp16; a
+    column range of a wider tensor will do).  Weights [n, k] get their scale for each output channel the same way."""
+    _on_device(x, codes, scales)
+    rows, k = x.shape
+    _floating("x", x)
+    _dense("codes", codes, torch.int8, rows, k)
+    _vector("scales", scales, torch.float32, rows)
+    if codes is None:
+        codes = _output((rows, k), torch.int8, x.device, stream)
+    if scales is None:
+        scales = _output((rows,), torch.float32, x.device, stream)
+    qmm_quantize_rows(x, x.dtype == torch.float16, _rows(x), codes, scales, rows, k, stream=stream)
+    return codes, scales
+
+
+def _out_i8(y: torch.Tensor | None, rows: int, n: int, out_fp16: bool, device, stream) -> torch.Tensor:
+    if y is None:
+        return _output((rows, n), torch.float16 if out_fp16 else torch.float32, device, stream)
+    _floating("y", y)
+    _dense("y", y, y.dtype, rows, n)
+    return y
+
+
+def gemm_i8(w: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales: torch.Tensor, y: torch.Tensor | None = None,
+            out_fp16: bool = False, stream=None) -> torch.Tensor:
+    """Y = (x_scales X) (w_scales W)^T: codes int8 W [n, k] and X [m, k], fp32 output, or fp16 with out_fp16."""
+    _on_device(w, w_scales, x, x_scales, y)
+    (n, k), m = w.shape, x.shape[0]
+    _dense("w", w, torch.int8, n, k)
+    _dense("x", x, torch.int8, m, k)
+    _vector("w_scales", w_scales, torch.float32, n)
+    _vector("x_scales", x_scales, torch.float32, m)
+    y = _out_i8(y, m, n, out_fp16, x.device, stream)
+    qmm_gemm_i8(w, w_scales, x, x_scales, y, y.dtype == torch.float16, m, n, k, stream=stream)
+    return y
+
+
+def _grouped_i8(stacks, x, x_scales, x_rows, offsets, y, out_fp16, stream):
+    """Checked operands of a product over rows grouped by expert: (y, rows, experts, n, k)."""
+    experts, n, k = stacks[0][0].shape
+    _on_device(x, x_scales, x_rows, offsets, y, *(t for s in stacks for t in s))
+    for w, s in stacks:
+        _dense("w", w, torch.int8, experts, n, k)
+        _vector("w_scales", s, torch.float32, experts * n)
+    _dense("x", x, torch.int8, x.shape[0], k)
+    _vector("x_scales", x_scales, torch.float32, x.shape[0])
+    _vector("x_rows", x_rows, torch.int32, 0)
+    _vector("offsets", offsets, torch.int32, experts + 1)
+    rows = x.shape[0] if x_rows is None else x_rows.numel()
+    return _out_i8(y, rows, n, out_fp16, x.device, stream), rows, experts, n, k
+
+
+def moe_i8(w: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales: torch.Tensor, x_rows: torch.Tensor | None,
+           offsets: torch.Tensor | None, y: torch.Tensor | None = None, out_fp16: bool = False, stream=None) -> torch.Tensor:
+    """8-bit products of rows grouped by expert: stacks w int8 [experts, n, k], w_scales [experts, n]; row p of expert e's
+    range is x[x_rows[p]] (x[p] if None).  One result row for each of x_rows (of x); those of no expert hold anything."""
+    y, rows, experts, n, k = _grouped_i8([(w, w_scales)], x, x_scales, x_rows, offsets, y, out_fp16, stream)
+    qmm_moe_gemm_i8(w, w_scales, x, x_scales, x_rows, x.shape[0], offsets, y, y.dtype == torch.float16, rows, experts, n, k,
+                    stream=stream)
+    return y
+
+
+def moe_swiglu_i8(gate: torch.Tensor, gate_scales: torch.Tensor, up: torch.Tensor, up_scales: torch.Tensor, x: torch.Tensor,
+                  x_scales: torch.Tensor, x_rows: torch.Tensor | None, offsets: torch.Tensor | None,
+                  h: torch.Tensor | None = None, out_fp16: bool = True, stream=None) -> torch.Tensor:
+    """h = silu(gate) * up of rows grouped by expert, both products in 8-bit integers in one launch."""
+    h, rows, experts, n, k = _grouped_i8([(gate, gate_scales), (up, up_scales)], x, x_scales, x_rows, offsets, h, out_fp16, stream)
+    qmm_moe_swiglu_i8(gate, gate_scales, up, up_scales, x, x_scales, x_rows, x.shape[0], offsets, h, h.dtype == torch.float16,
+                      rows, experts, n, k, stream=stream)
+    return h
 
 
 def _rows(t: torch.Tensor) -> int:
