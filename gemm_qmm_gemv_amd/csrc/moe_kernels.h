@@ -56,6 +56,7 @@ struct GemmI8Args {
     int64_t n;
     int k, experts, cus;
     bool y16;
+    bool past_caches;            // y is written past the caches
 };
 hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t st);
 
