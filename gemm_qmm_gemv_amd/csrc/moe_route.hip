@@ -9,9 +9,11 @@
 //
 // A choice hangs on the last bits of its scores, so it is made on numbers that
 // never run together: without a bias the order of the scores is that of the
-// logits, which are compared as they are; with one, scores are formed in 64
+// logits, which are compared as they are; with one, and for groups by the sum of
+// two, on scores in fp32 where they lie far enough apart for that, else in 64
 // bits.  Keys are whole numbers in the order of the values, so that a place that
 // is taken (or not there) has a key below all of them.
+#include <algorithm>
 #include <type_traits>
 
 #include "layer_device.h"
@@ -503,11 +505,12 @@ __device__ __forceinline__ int sums_before(int experts, int* part, N own, To to)
     return base;
 }
 
-// Tokens of one work-group: 16 while many work-groups are quicker than few with
-// more rounds (1024 tokens of 256 experts: 13.6 us against 24), 64 beyond, as
-// the second launch reads all rows of counts in every work-group (16384 tokens of
-// 128 experts: 17.3 us against 21.9 with rows of 16 tokens).
-int block_tokens(int64_t tokens) { return tokens <= ROUTE_WAVES ? 16 : 64; }
+// Tokens of one work-group: few for short batches, so that waves do not wait for
+// each other's instructions (37 tokens of 256 experts in groups: 12.6 us with 4,
+// 13.3 with 8, 15.7 with 16; 1024 of them 15.2 with 8, 17.2 with 16), more for
+// longer ones, as the second launch reads all rows of counts in every work-group
+// (16384 tokens of 128 experts: 17.3 us with 64, 21.9 with 16).
+int block_tokens(int64_t tokens) { return tokens <= 256 ? 4 : tokens <= 2048 ? 8 : tokens <= ROUTE_WAVES ? 16 : 64; }
 
 // A work-group takes `block` tokens, blockDim / L of them at a time (ONE: it is
 // the only one).  Ranks within an expert come from a mask per expert with a bit
@@ -525,6 +528,7 @@ __global__ void __launch_bounds__(1024) route_kernel(RouteArgs a, int block) {
     __syncthreads();
     for (int t0 = 0; t0 < here; t0 += threads / L) {
         const int t = t0 + tid / L;
+        if (L == 64 && t >= here) break;  // a whole wave
         const int64_t token = first + (t < here ? t : 0);
         Chosen c = choose<L, PER, MODE>(a, token, lane);
         if (t < here && lane < a.top_k) {
@@ -693,7 +697,9 @@ template <int L, int PER, Mode MODE>
 hipError_t launch(const RouteArgs& a, hipStream_t st) {
     constexpr int AT_ONCE = 1024 / L;
     if (a.tokens <= AT_ONCE) {
-        const int threads = a.tokens * L < 64 ? 64 : (int)((a.tokens * L + 63) / 64 * 64);
+        // Four waves at least, for what is done for each expert (one token of 256
+        // experts: 5.1 us, 6.1 with one wave).
+        const int threads = a.tokens * L < 256 ? 256 : (int)((a.tokens * L + 63) / 64 * 64);
         const size_t lds = (size_t)a.experts * 12 + (size_t)AT_ONCE * a.top_k * 8;
         route_kernel<L, PER, MODE, true><<<dim3(1), dim3(threads), lds, st>>>(a, AT_ONCE);
         return hipGetLastError();
@@ -727,7 +733,9 @@ hipError_t launch_mode(const RouteArgs& a, hipStream_t st) {
 size_t route_workspace(int64_t tokens, int experts) {
     if (tokens <= ROUTE_ONE) return 0;
     const int block = block_tokens(tokens);
-    const int64_t blocks = (tokens + block - 1) / block;
+    // (What does for these tokens does for fewer, which may have more rows of counts.)
+    const int64_t fewer = tokens > 2048 ? 256 : tokens > 256 ? 64 : 0;
+    const int64_t blocks = std::max((tokens + block - 1) / block, fewer);
     return (size_t)(count_bytes(blocks, experts) + (blocks > CHUNKED ? 4 * count_bytes((blocks + CHUNK - 1) / CHUNK, experts) : 0));
 }
 
@@ -736,8 +744,9 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
     // experts: 4.5 us against 6.3 with 16 lanes); four tokens to a wave take
     // fewer instructions in all and are quicker once the device is full (16384
     // tokens of 128 experts, ids only: 9.3 us against 13.7), and where they save
-    // the second launch (37 tokens: 8.4 us against 10.4).
-    const bool one = a.tokens > ROUTE_ONE && a.tokens <= ROUTE_ONE_16 && !a.bias && a.groups == 1;
+    // the second launch (64 experts: 64 tokens 7.7 us, 8.9 with a wave each; 128:
+    // 48 tokens 8.9, 9.0, but 64 tokens 10.6, 9.1).
+    const bool one = a.tokens > ROUTE_ONE && a.tokens <= (a.experts <= 64 ? ROUTE_ONE_16 : 48) && !a.bias && a.groups == 1;
     if ((a.tokens > ROUTE_WAVES || one) && a.top_k <= 16 && a.groups <= 16) {
         if (a.experts <= 64) return launch_mode<16, 4>(a, st);
         if (a.experts <= 128) return launch_mode<16, 8>(a, st);

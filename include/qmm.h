@@ -511,8 +511,8 @@ QMM_API qmm_status qmm_attn_prompt(const void *q, const void *k, const void *v,
  *   pair_token int32, pair_weight fp32 [tokens * top_k], or NULL: token and
  *     weight of each row; behind the last row they are left as they were.
  *   workspace: device scratch of qmm_moe_route_workspace_bytes(), 16-byte aligned,
- *     needed only to group (else QMM_ERR_INVALID_ARGUMENT); it may hold anything.
- *     Calls that overlap need a workspace each.
+ *     needed only to group (else QMM_ERR_INVALID_ARGUMENT); it may hold anything,
+ *     and one for some tokens serves fewer.  Calls that overlap need a workspace each.
  * n_experts at most 1024, n_groups and top_k at most 64, tokens below 2^24, else
  * QMM_ERR_UNSUPPORTED.  tokens 0: the offsets are set to 0.  No output may
  * overlap an input or another output.                                       */

@@ -204,6 +204,14 @@ def test_without_groups_and_without_tokens():
     assert (out["offsets"] == UNTOUCHED).all()
 
 
+@pytest.mark.parametrize("tokens", [16, 17, 48, 49, 64, 255, 256, 257, 2047, 2049])
+@pytest.mark.parametrize("experts,grouped", [(64, False), (128, False), (256, True)])
+def test_where_the_launch_changes(tokens, experts, grouped):
+    rng = np.random.default_rng(7 * tokens + experts)
+    how = dict(kind="sigmoid", groups=8, top_groups=4, best=2, bias=0.1 * normal(rng, experts)) if grouped else {}
+    run(normal(rng, tokens, experts), "launches", top_k=8, **how)
+
+
 @pytest.mark.parametrize("tokens,experts", [(5000, 128), (4096, 100), (4097, 384), (9001, 8), (16384, 40), (16385, 129), (70001, 20), (262145, 16)])
 def test_many_tokens(tokens, experts):
     # Against the oracle for a sample's choices, and the grouping whole.

@@ -62,6 +62,11 @@ def test_route_workspace():
     assert sizes[0] == 0 and all(s > 0 for s in sizes[1:])
 
 
+def test_route_workspace_serves_fewer_tokens():
+    sizes = [qmm.qmm_moe_route_workspace_bytes(t, 100, 4) for t in (*range(1, 300), 2047, 2048, 2049, 2064, 4095, 4096, 4097, 8192, 16384, 16448, 1 << 18)]
+    assert sizes == sorted(sizes)
+
+
 def quantize(x=A16, f16=True, stride=64, codes=A16, scales=A16, rows=3, k=64):
     return status(qmm.qmm_quantize_rows, x, f16, stride, codes, scales, rows, k)
 
