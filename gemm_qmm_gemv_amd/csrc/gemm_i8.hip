@@ -225,10 +225,12 @@ __device__ __forceinline__ void lds_barrier() {
 
 // Where each expert's row tiles begin: table [2][experts + 1], filled by the
 // first wave: tiles before (behind the last expert: all), offsets inside the
-// rows.
+// rows.  (Offsets that fall and rise again may count more tiles than a launch can
+// have; 2^30 is more than any has.)
 __device__ __forceinline__ void fill_table(const GemmI8Args& a, int bm, int* table) {
+    constexpr u32 MOST = 1u << 30;
     const int lane = threadIdx.x & 63;
-    int before = 0;
+    u32 before = 0;
     for (int e0 = 0; e0 < a.experts; e0 += 64) {
         const int e = e0 + lane;
         int64_t lo = 0, hi = 0;
@@ -238,20 +240,21 @@ __device__ __forceinline__ void fill_table(const GemmI8Args& a, int bm, int* tab
             lo = lo < 0 ? 0 : lo > a.rows ? a.rows : lo;
             hi = hi < lo ? lo : hi > a.rows ? a.rows : hi;
         }
-        const int n = (int)((hi - lo + bm - 1) / bm);
-        int sum = n;
+        const u32 n = (u32)((hi - lo + bm - 1) / bm);
+        u32 sum = n;
         for (int d = 1; d < 64; d *= 2) {
-            const int x = __shfl_up(sum, d, 64);
+            const u32 x = __shfl_up(sum, d, 64);
             if (lane >= d) sum += x;
         }
         if (e < a.experts) {
-            table[e] = before + sum - n;
+            table[e] = (int)(before + sum - n < MOST ? before + sum - n : MOST);
             table[a.experts + 1 + e] = (int)lo;
             if (e == a.experts - 1) table[a.experts + 1 + a.experts] = (int)hi;
         }
         before += __shfl(sum, 63, 64);
+        before = before < MOST ? before : MOST;
     }
-    if (lane == 0) table[a.experts] = before;
+    if (lane == 0) table[a.experts] = (int)before;
 }
 
 struct Tile {
@@ -393,7 +396,9 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
     if (a.offsets) {
         if (wave == 0) fill_table(a, BM, table);
         __syncthreads();
+        const int64_t most = a.rows / BM + (a.rows < a.experts ? a.rows : a.experts);  // as the host has it
         rtiles = uniform(table[a.experts]);
+        rtiles = rtiles < most ? rtiles : (int)most;
     } else {
         rtiles = (int)((a.rows + BM - 1) / BM);
     }

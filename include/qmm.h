@@ -534,7 +534,7 @@ QMM_API size_t qmm_moe_route_workspace_bytes(int64_t tokens, int n_experts, int 
  *   y fp32 [tokens][n] (written).
  * Sums are fp32, in the order of j, the residual last.  top_k at most 64, tokens below 2^24,
  * n below 2^22, else QMM_ERR_UNSUPPORTED.  Pointers aligned to their elements;
- * 16-byte aligned rows (n a multiple of 8) are faster.                      */
+ * n a multiple of 8 (of 4 for fp32 rows) and 16-byte aligned pointers are faster. */
 QMM_API qmm_status qmm_moe_gather(const void *rows, int rows_fp16, const int32_t *pair_row,
                                   const float *weights, const float *residual, float *y,
                                   int64_t tokens, int top_k, int64_t p_rows, int64_t n,
@@ -570,7 +570,8 @@ QMM_API qmm_status qmm_gemm_i8(const int8_t *w, const float *w_scales, const int
  * x_rows[p] (int32 [p_rows]; p if NULL) of x_rows_count.  expert_offsets, rows
  * with an activation index out of range (NaN) and rows that no expert covers
  * (left as they were) are as for qmm_moe_gemm; expert_offsets NULL with one
- * expert: all rows are its.                                                 */
+ * expert: all rows are its.  n_experts at most 1024, p_rows below 2^31 (else
+ * QMM_ERR_UNSUPPORTED).                                                     */
 QMM_API qmm_status qmm_moe_gemm_i8(const int8_t *w, const float *w_scales, const int8_t *x,
                                    const float *x_scales, const int32_t *x_rows,
                                    int64_t x_rows_count, const int32_t *expert_offsets, void *y,
