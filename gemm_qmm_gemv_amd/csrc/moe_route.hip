@@ -26,9 +26,11 @@ constexpr float INF = __builtin_huge_valf();
 // Tokens that one work-group routes and places in one launch: what it holds at
 // once, with a wave or 16 lanes for each.
 constexpr int ROUTE_ONE = 16, ROUTE_ONE_16 = 64;
-// Up to this many tokens get a wave each, and a work-group takes 16 of them.
+// Up to this many tokens get a wave each.
 constexpr int ROUTE_WAVES = 4096;
-// Rows of counts that are summed up for the second launch, if there are more.
+// Tokens that one work-group places.
+constexpr int PLACE = 64;
+// Rows of counts that are summed up for the second launch, if there are more than CHUNKED.
 constexpr int CHUNK = 64, CHUNKED = 256;
 
 __device__ __forceinline__ int order_key(float v) {
@@ -505,12 +507,16 @@ __device__ __forceinline__ int sums_before(int experts, int* part, N own, To to)
     return base;
 }
 
-// Tokens of one work-group: few for short batches, so that waves do not wait for
-// each other's instructions (37 tokens of 256 experts in groups: 12.6 us with 4,
-// 13.3 with 8, 15.7 with 16; 1024 of them 15.2 with 8, 17.2 with 16), more for
-// longer ones, as the second launch reads all rows of counts in every work-group
-// (16384 tokens of 128 experts: 17.3 us with 64, 21.9 with 16).
-int block_tokens(int64_t tokens) { return tokens <= 256 ? 4 : tokens <= 2048 ? 8 : tokens <= ROUTE_WAVES ? 16 : 64; }
+// Tokens of one work-group: few, so that waves do not wait for each other's
+// instructions (37 tokens of 256 experts in groups: 12.6 us with 4, 13.3 with 8,
+// 15.7 with 16; 4097 of 256: 18.4 with 32, 25.9 with 64), but no more than 256
+// work-groups, as the second launch reads all rows of counts in each of its own
+// (16384 tokens of 128: 17.3 us with 64, 21.9 with 16).
+int block_tokens(int64_t tokens) {
+    int block = 4;
+    while (block < PLACE && (tokens + block - 1) / block > CHUNKED) block *= 2;
+    return block;
+}
 
 // A work-group takes `block` tokens, blockDim / L of them at a time (ONE: it is
 // the only one).  Ranks within an expert come from a mask per expert with a bit
@@ -598,11 +604,10 @@ __global__ void __launch_bounds__(256) route_sums_kernel(const uint8_t* counts, 
     for (int e = tid; e < width; e += 256) sums[(int64_t)blockIdx.x * width + e] = all_of[e];
 }
 
-// Last launch where several work-groups routed: each takes 64 tokens, adds up
+// Last launch where several work-groups routed: each takes PLACE tokens, adds up
 // what the experts got before, and places its pairs.  Counts (`blocks` rows, of
 // `block` tokens each) are read 16 experts a thread, rows of them side by side;
 // where there are sums of CHUNK rows, those and the rows of the own chunk.
-constexpr int PLACE = 64;
 __global__ void __launch_bounds__(256) route_place_kernel(RouteArgs a, int block, int blocks, const u32* sums) {
     extern __shared__ uint64_t mask[];  // [experts], then [2][width]: rows before this work-group, all rows
     __shared__ int part[4];
@@ -734,7 +739,7 @@ size_t route_workspace(int64_t tokens, int experts) {
     if (tokens <= ROUTE_ONE) return 0;
     const int block = block_tokens(tokens);
     // (What does for these tokens does for fewer, which may have more rows of counts.)
-    const int64_t fewer = tokens > 2048 ? 256 : tokens > 256 ? 64 : 0;
+    const int64_t fewer = tokens > 4 * CHUNKED ? CHUNKED : 0;
     const int64_t blocks = std::max((tokens + block - 1) / block, fewer);
     return (size_t)(count_bytes(blocks, experts) + (blocks > CHUNKED ? 4 * count_bytes((blocks + CHUNK - 1) / CHUNK, experts) : 0));
 }
@@ -746,10 +751,14 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
     // tokens of 128 experts, ids only: 9.3 us against 13.7), and where they save
     // the second launch (64 experts: 64 tokens 7.7 us, 8.9 with a wave each; 128:
     // 48 tokens 8.9, 9.0, but 64 tokens 10.6, 9.1).
-    const bool one = a.tokens > ROUTE_ONE && a.tokens <= (a.experts <= 64 ? ROUTE_ONE_16 : 48) && !a.bias && a.groups == 1;
+    const bool one = a.experts <= 128 && a.tokens > ROUTE_ONE && a.tokens <= (a.experts <= 64 ? ROUTE_ONE_16 : 48) && !a.bias && a.groups == 1;
     if ((a.tokens > ROUTE_WAVES || one) && a.top_k <= 16 && a.groups <= 16) {
         if (a.experts <= 64) return launch_mode<16, 4>(a, st);
         if (a.experts <= 128) return launch_mode<16, 8>(a, st);
+        // 16 experts a lane only where the choice is on logits (16384 tokens of 256:
+        // 25.5 us against 29.6); with scores beside them registers run out (with a
+        // bias 44.6 against 38.8).
+        if (a.experts <= 256 && !a.bias && (a.groups == 1 || a.group_best == 1)) return launch<16, 16, LOGITS>(a, st);
     }
     if (a.experts <= 64) return launch_mode<64, 1>(a, st);
     if (a.experts <= 128) return launch_mode<64, 2>(a, st);

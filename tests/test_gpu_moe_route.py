@@ -212,6 +212,15 @@ def test_where_the_launch_changes(tokens, experts, grouped):
     run(normal(rng, tokens, experts), "launches", top_k=8, **how)
 
 
+@pytest.mark.parametrize("tokens", [1023, 1025, 4097, 8193])
+@pytest.mark.parametrize("how", ["best", "groups", "pairs", "biased"])
+def test_long_batches_of_256_experts(tokens, how):
+    rng = np.random.default_rng(tokens)
+    more = {"best": {}, "groups": dict(groups=8, top_groups=3), "pairs": dict(groups=16, top_groups=4, best=2),
+            "biased": dict(kind="sigmoid", bias=0.1 * normal(rng, 250))}[how]
+    run(normal(rng, tokens, 250 if how in ("best", "biased") else 256), how, top_k=6, keep=dev(np.asarray(rng.random(tokens) < 0.9, dtype=np.uint8)), **more)
+
+
 @pytest.mark.parametrize("tokens,experts", [(5000, 128), (4096, 100), (4097, 384), (9001, 8), (16384, 40), (16385, 129), (70001, 20), (262145, 16)])
 def test_many_tokens(tokens, experts):
     # Against the oracle for a sample's choices, and the grouping whole.
