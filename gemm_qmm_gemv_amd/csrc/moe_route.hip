@@ -4,8 +4,8 @@
 //   the top_groups groups of highest score stay (a group's score: the sum of
 //   its group_best highest c), of their experts the top_k of highest c,
 //   w = s[chosen] [/ sum over the chosen] * scale,
-// then a counting sort of the (token, expert) pairs by expert, within an expert
-// by token.
+// in fp32 from the logits of the chosen, then a counting sort of the (token,
+// expert) pairs by expert, within an expert by token.
 //
 // A choice hangs on the last bits of its scores, so it is made on numbers that
 // never run together: without a bias the order of the scores is that of the
@@ -13,6 +13,13 @@
 // two, on scores in fp32 where they lie far enough apart for that, else in 64
 // bits.  Keys are whole numbers in the order of the values, so that a place that
 // is taken (or not there) has a key below all of them.
+//
+// Short batches are one chain of waits and lane moves: one token of 128 experts
+// 4.3 us (an empty launch: 1.6), 37 of 256 in groups with a bias 8.5 and 4.8
+// for the placing; a choice left open costs such a call 5 us more.  Long ones
+// are bound by vector instructions (16384 tokens of 128: 10.3 us at 72 % busy,
+// 256 in groups with a bias 42 us at 84 %; 262144 of 128: 133 us, 81 %); the
+// placing waits for memory and LDS (8.9 us; 59 for the longest).
 #include <algorithm>
 #include <type_traits>
 
@@ -30,7 +37,8 @@ constexpr int ROUTE_ONE = 16, ROUTE_ONE_16 = 64;
 constexpr int ROUTE_WAVES = 4096;
 // Tokens that one work-group places.
 constexpr int PLACE = 64;
-// Rows of counts that are summed up for the second launch, if there are more than CHUNKED.
+// Rows of counts that are summed up for the second launch, if there are more
+// than CHUNKED.
 constexpr int CHUNK = 64, CHUNKED = 256;
 
 __device__ __forceinline__ int order_key(float v) {
