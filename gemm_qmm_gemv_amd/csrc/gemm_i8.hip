@@ -425,8 +425,25 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
     }
     // Each of the 8 dies (work-group i runs on die i % 8) takes neighbouring tiles.
     const int tiles = rtiles * ncols, per = (tiles + 7) / 8, base = (int)(blockIdx.x % 8) * per;
-    const int count = tiles - base < per ? tiles - base : per, hop = (int)(gridDim.x / 8);
+    int count = tiles - base < per ? tiles - base : per;
+    const int hop = (int)(gridDim.x / 8);
     int t = (int)(blockIdx.x / 8);
+    // A last round for at most half of the work-groups is cut into tiles of half
+    // the rows, for twice as many (4500 x 4096 of 4096: 98 -> 91 us; 4096 tokens
+    // through 128 experts' down projection 133 -> 129).
+    const int whole = count / hop * hop, rest = count - whole;
+    const bool halves = whole > 0 && 2 * rest <= hop;
+    if (halves) count += rest;
+    const auto nth = [&](int i) {
+        if (!halves || i < whole) return tile_at(a, base + i, rtiles, ncols, BM, BN, table);
+        Tile q = tile_at(a, base + whole + (i - whole) / 2, rtiles, ncols, BM, BN, table);
+        const int cut = q.to - q.from < BM / 2 ? q.to : q.from + BM / 2;
+        if ((i - whole) % 2)
+            q.from = cut;
+        else
+            q.to = cut;
+        return q;
+    };
     if (t >= count) return;
 
     const u32 wbytes = (u32)(a.n * a.k), xbytes = (u32)(a.x_rows_count * a.k);
@@ -513,7 +530,7 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
             }
     };
 
-    Tile cur = tile_at(a, base + t, rtiles, ncols, BM, BN, table);
+    Tile cur = nth(t);
     u32 off[LOADS];
     int stage = 0, which = 0;
     {
@@ -551,7 +568,7 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
         int x = -1;
         float s[SCALES];
         if (more) {
-            next = tile_at(a, base + t + hop, rtiles, ncols, BM, BN, table);
+            next = nth(t + hop);
             x = fetch_row(next);
             if (steps == 1) {
                 if (tid < BM) rows_of[tid] = x;
@@ -605,8 +622,8 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
             stage ^= 1;
             multiply(odd);
         } else {
-            // An expert's last tile, and none of its rows are this wave's: it only
-            // loads, in step with the others.
+            // A tile of fewer rows, none of which are this wave's: it only loads, in
+            // step with the others.
             for (int st = 0; st + 2 < steps; ++st) {
                 loads_barrier();
                 load(off, st + 2, stage);

@@ -108,6 +108,13 @@ def test_many_tiles(m, n, k, f16):
     assert ((y[:m].double() - want).abs() <= bound).all()
 
 
+# A few tiles more than the work-groups take at once, of 64, 128 and 256 rows and columns, of full and of few rows.
+@pytest.mark.parametrize("m,n", [(4500, 4096), (4100, 4096), (4353, 4096), (8200, 8192), (3000, 2900), (2049, 4096), (1700, 1950), (1600, 2000)])
+@pytest.mark.parametrize("k", [96, 256, 1056])
+def test_a_last_round_of_few_tiles(m, n, k):
+    test_many_tiles(m, n, k, k == 256)
+
+
 @pytest.mark.parametrize("glu", [False, True])
 @pytest.mark.parametrize("experts,n,k,mean", [(3, 1000, 160, 700), (40, 512, 96, 90), (128, 520, 64, 30), (2, 2048, 128, 3000), (8, 768, 2048, 500), (100, 256, 32, 200)])
 def test_many_grouped_tiles(glu, experts, n, k, mean):
@@ -223,6 +230,13 @@ def test_groups(counts, glu, x_rows):
 @pytest.mark.parametrize("per", [1, 20, 90])
 def test_groups_of_other_sizes(glu, n, k, per):
     grouped(3, [per, 0, per + 5], n, k, True, glu)
+
+
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("experts,n,k,mean", [(128, 768, 96, 256), (128, 700, 160, 100), (64, 1001, 64, 300), (16, 2048, 288, 520), (16, 2200, 128, 500)])
+def test_last_rounds_of_grouped_tiles(glu, experts, n, k, mean):
+    for shift in (0, 40, 90):
+        test_many_grouped_tiles(glu, experts, n, k, mean + shift)
 
 
 @pytest.mark.parametrize("glu", [False, True])
