@@ -238,6 +238,13 @@ __device__ __forceinline__ void loads_barrier() {
     __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0), lgkmcnt(0)
     asm volatile("s_barrier" ::: "memory");
 }
+// The same behind all but the newest N of its loads.
+template <int N>
+__device__ __forceinline__ void older_loads_barrier() {
+    static_assert(N < 64, "what the counter holds");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4);  // vmcnt(N), lgkmcnt(0)
+    asm volatile("s_barrier" ::: "memory");
+}
 // The same without the loads.
 __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_s_waitcnt(15 | 3 << 14 | 7 << 4);  // lgkmcnt(0)
@@ -390,7 +397,7 @@ __device__ __forceinline__ void store_block(const GemmI8Args& a, const Tile& t, 
     }
 }
 
-template <int WM, int WN, int MF, int NF, bool GLU>
+template <int WM, int WN, int MF, int NF, bool GLU, int STAGES>
 struct TileShape {
     static constexpr int S = GLU ? 2 : 1, WAVES = WM * WN, T = 64 * WAVES;
     static constexpr int BM = 32 * MF * WM, BN = 32 * NF * WN;  // columns of each stack
@@ -399,15 +406,20 @@ struct TileShape {
     static constexpr int SCALES = (ROWS + T - 1) / T;  // per thread
     static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "a load brings rows of one side in all waves");
     static_assert(BM <= T, "a thread for each row");
-    static_assert(WAVES * OUT <= STAGE, "outputs pass through a stage's place");
+    static_assert(WAVES * OUT <= STAGE * (STAGES - 1), "outputs pass through the stages that are read");
 };
 
-template <int WM, int WN, int MF, int NF, bool GLU, int OCC>
+// STAGES 2: as above.  More: a work-group has one tile, and a step in flight for
+// each stage from the start, for launches of few tiles, where the wait for the
+// next step is what counts (256 rows, 2048 columns of 8192: tiles of 64 x 64 in
+// four stages 19.6 us, in two 30; 512 rows, 4096 of 4096: 128 x 64 in three 15.5,
+// the best of two 23).
+template <int WM, int WN, int MF, int NF, bool GLU, int OCC, int STAGES>
 __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a) {
-    using Shape = TileShape<WM, WN, MF, NF, GLU>;
+    using Shape = TileShape<WM, WN, MF, NF, GLU, STAGES>;
     constexpr int S = Shape::S, BM = Shape::BM, BN = Shape::BN, ROWS = Shape::ROWS, STAGE = Shape::STAGE, LOADS = Shape::LOADS;
     constexpr int T = Shape::T, SCALES = Shape::SCALES, WAVES = Shape::WAVES;
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[STAGES * STAGE];
     __shared__ __attribute__((aligned(16))) float scales[2 * ROWS];  // of two tiles
     __shared__ int rows_of[BM];
     __shared__ int table[2 * (I8_EXPERTS + 1)];
@@ -530,8 +542,83 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
             }
     };
 
+    i32x16 acc[S][NF][MF];
+    const auto clear = [&] {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int j = 0; j < MF; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[s][i][j][v] = 0;
+    };
+    const auto multiply = [&](const Pieces& f) {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int j = 0; j < MF; ++j)
+                    acc[s][i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[s][i], f.x[j], acc[s][i][j], 0, 0, 0);
+    };
+    Pieces even, odd;
+    // Quarters of a stage: all but the last one's products.
+    const auto quarters = [&](int stage) {
+        read(odd, stage, 1);
+        multiply(even);
+        read(even, stage, 2);
+        multiply(odd);
+        read(odd, stage, 3);
+        multiply(even);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto put = [&](const Tile& q, int which, unsigned char* through) {
+        unsigned char* const mine = through + wave * OUT;
+        const float* const sx = scales + which * ROWS;
+        const float* const sg = sx + BM + wn * NF * 32;
+        if (a.y16)
+            store_block<f16, NF, MF, GLU>(a, q, wm * MF * 32, (int64_t)q.n0 + wn * NF * 32, sx, sg, sg + BN, acc, mine);
+        else
+            store_block<float, NF, MF, GLU>(a, q, wm * MF * 32, (int64_t)q.n0 + wn * NF * 32, sx, sg, sg + BN, acc, mine);
+    };
+
     Tile cur = nth(t);
     u32 off[LOADS];
+    if constexpr (STAGES > 2) {
+        float s[SCALES];
+        const int x = fetch_row(cur);
+        if (tid < BM) rows_of[tid] = x;
+        __syncthreads();
+        fetch_scales(cur, s);
+        offsets(cur, off);
+        for (int i = 0; i < STAGES; ++i) load(off, i, i);
+        older_loads_barrier<(STAGES - 1) * LOADS>();
+        clear();
+        // Steps behind the last one are zeros that nothing reads.
+        const auto turn = [](int stage) { return stage + 1 == STAGES ? 0 : stage + 1; };
+        if (wm * MF * 32 < cur.to - cur.from) {
+            read(even, 0, 0);
+            for (int st = 0, stage = 0; st < steps; ++st) {
+                quarters(stage);
+                older_loads_barrier<(STAGES - 2) * LOADS>();
+                load(off, st + STAGES, stage);
+                stage = turn(stage);
+                read(even, stage, 0);
+                multiply(odd);
+            }
+        } else {
+            for (int st = 0, stage = 0; st < steps; ++st) {
+                older_loads_barrier<(STAGES - 2) * LOADS>();
+                load(off, st + STAGES, stage);
+                stage = turn(stage);
+            }
+        }
+        keep_scales(s, 0);
+        loads_barrier();
+        put(cur, 0, lds);
+        return;
+    }
     int stage = 0, which = 0;
     {
         float s[SCALES];
@@ -545,24 +632,7 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
     }
     loads_barrier();
     for (;;) {
-        i32x16 acc[S][NF][MF];
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int i = 0; i < NF; ++i)
-#pragma unroll
-                for (int j = 0; j < MF; ++j)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) acc[s][i][j][v] = 0;
-        const auto multiply = [&](const Pieces& f) {
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-#pragma unroll
-                for (int i = 0; i < NF; ++i)
-#pragma unroll
-                    for (int j = 0; j < MF; ++j)
-                        acc[s][i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[s][i], f.x[j], acc[s][i][j], 0, 0, 0);
-        };
+        clear();
         const bool more = t + hop < count;
         Tile next{};
         int x = -1;
@@ -588,20 +658,10 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
         else
             bring_next(stage ^ 1);
         if (wm * MF * 32 < cur.to - cur.from) {
-            Pieces even, odd;
             read(even, stage, 0);
-            const auto quarters = [&] {
-                read(odd, stage, 1);
-                multiply(even);
-                read(even, stage, 2);
-                multiply(odd);
-                read(odd, stage, 3);
-                multiply(even);
-                __builtin_amdgcn_sched_barrier(0);
-            };
             // Behind the barrier the other stage is there, and this one is read no more.
             for (int st = 0; st + 2 < steps; ++st) {
-                quarters();
+                quarters(stage);
                 loads_barrier();
                 load(off, st + 2, stage);
                 stage ^= 1;
@@ -609,7 +669,7 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
                 multiply(odd);
             }
             if (steps > 1) {
-                quarters();
+                quarters(stage);
                 if (tid < BM) rows_of[tid] = x;
                 loads_barrier();
                 bring_next(stage);
@@ -617,7 +677,7 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
                 read(even, stage, 0);
                 multiply(odd);
             }
-            quarters();
+            quarters(stage);
             loads_barrier();
             stage ^= 1;
             multiply(odd);
@@ -639,13 +699,7 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
             stage ^= 1;
         }
         if (more) keep_scales(s, which ^ 1);
-        unsigned char* const mine = lds + (stage ^ 1) * STAGE + wave * OUT;
-        const float* const sx = scales + which * ROWS;
-        const float* const sg = sx + BM + wn * NF * 32;
-        if (a.y16)
-            store_block<f16, NF, MF, GLU>(a, cur, wm * MF * 32, (int64_t)cur.n0 + wn * NF * 32, sx, sg, sg + BN, acc, mine);
-        else
-            store_block<float, NF, MF, GLU>(a, cur, wm * MF * 32, (int64_t)cur.n0 + wn * NF * 32, sx, sg, sg + BN, acc, mine);
+        put(cur, which, lds + (stage ^ 1) * STAGE);
         if (!more) return;
         lds_barrier();  // before the next step's loads go where the sums passed
         cur = next;
@@ -670,40 +724,50 @@ hipError_t launch_rows(const GemmI8Args& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <int WM, int WN, int MF, int NF, bool GLU, int OCC>
+template <int WM, int WN, int MF, int NF, bool GLU, int OCC, int STAGES = 2>
 hipError_t launch_tile(const GemmI8Args& a, hipStream_t st) {
-    using Shape = TileShape<WM, WN, MF, NF, GLU>;
+    using Shape = TileShape<WM, WN, MF, NF, GLU, STAGES>;
     const int64_t tiles = row_tiles(a, Shape::BM) * ((a.n + Shape::BN - 1) / Shape::BN);
-    if (tiles > 0x3fffffff) return hipErrorInvalidConfiguration;
-    // As many work-groups as the device holds at once, the same for every die.
-    int64_t grid = (int64_t)a.cus * std::max(1, 4 * OCC / Shape::WAVES) / 8 * 8;
-    if (grid > tiles) grid = (tiles + 7) / 8 * 8;
+    if (tiles > (STAGES > 2 ? 0x3fffff : 0x3fffffff)) return hipErrorInvalidConfiguration;
+    // As many work-groups as the device holds at once, or one for each tile; the
+    // same for every die.
+    int64_t grid = STAGES > 2 ? tiles : (int64_t)a.cus * std::max(1, 4 * OCC / Shape::WAVES) / 8 * 8;
+    if (grid >= tiles) grid = (tiles + 7) / 8 * 8;
     if (grid < 8) grid = 8;
-    tile_i8_kernel<WM, WN, MF, NF, GLU, OCC><<<dim3((unsigned)grid), dim3(Shape::T), 0, st>>>(a);
+    tile_i8_kernel<WM, WN, MF, NF, GLU, OCC, STAGES><<<dim3((unsigned)grid), dim3(Shape::T), 0, st>>>(a);
     return hipGetLastError();
 }
 
-// What a launch of a tile kernel takes, in microseconds, from timings of 84
-// dense shapes (1 to 1024 rows, 1000 to 16384 columns of 512 to 8192 codes) and
-// 44 grouped ones (16 and 128 experts): `begin` for a tile's ends and `one` for a
-// step of 128 codes while every tile has a compute unit for itself; `full` for a
-// step once all places are taken, and in proportion beyond.
+// What a launch of a tile kernel takes, in microseconds, fitted to timings of 176
+// dense shapes (17 to 8192 rows, 1000 to 16384 columns of 512 to 8192 codes) and
+// 320 grouped ones (8 to 128 experts): `begin` for a tile's ends (`grouped` once,
+// where rows are looked for) and `one` for a step of 128 codes while every tile
+// has a compute unit for itself; `full` for a step once all places are taken, and
+// in proportion between; `last`, how much a round that is only begun costs beyond
+// its share, and less after many uneven ones; `part`, what an expert's last tile,
+// which lacks rows, costs beside a full one.  The kernel taken is within 1.1 % of
+// the best on average, and within 10 % in 481 of the 496.
 struct TileCost {
     int bm, bn, places;  // work-groups that a compute unit holds
-    double begin, one, full;
+    double begin, grouped, one, full, last, part;
 };
-constexpr TileCost COST_64{64, 64, 3, 2.5, 0.5, 0.85}, COST_64_GATED{64, 64, 2, 3.0, 0.85, 1.1};
-constexpr TileCost COST_128{128, 128, 2, 2.5, 0.72, 1.2}, COST_128_GATED{128, 64, 2, 2.5, 0.72, 1.2};
-constexpr TileCost COST_256{256, 256, 1, 5.0, 1.2, 1.78}, COST_256_GATED{256, 128, 1, 5.0, 1.2, 1.78};
+// DEEP: a step in flight for each of several stages.
+constexpr TileCost DEEP_64{64, 64, 2, 4.4, 1.1, 0.245, 0.45, 0.14, 0.83}, DEEP_128{128, 64, 1, 4.8, 0.5, 0.25, 0.35, 0.66, 0.66};
+constexpr TileCost COST_64{64, 64, 3, 3.45, 1.6, 0.5, 0.76, 0.3, 0.8}, COST_128{128, 128, 2, 4.4, 1.0, 0.74, 1.05, 0.59, 0.71};
+constexpr TileCost COST_256{256, 256, 1, 7.8, 0.0, 1.48, 1.77, 0.52, 0.6};
+constexpr TileCost DEEP_64_GATED{64, 64, 1, 4.8, 1.2, 0.21, 0.5, 0.63, 0.66}, COST_64_GATED{64, 64, 2, 3.1, 1.9, 0.75, 0.87, 0.15, 1.2};
+constexpr TileCost COST_128_GATED{128, 64, 2, 3.6, 2.0, 0.8, 1.11, 0.15, 1.0}, COST_256_GATED{256, 128, 1, 8.1, 1.9, 0.6, 1.55, 0.38, 0.83};
 
-double tile_time(const GemmI8Args& a, const TileCost& c, double per, double met) {
-    // Grouped: every expert that has rows ends in a tile that is half empty on average.
-    const double rt = a.offsets ? std::max(met, per * a.experts / c.bm + met / 2) : (double)((a.rows + c.bm - 1) / c.bm);
-    const double tiles = rt * (double)((a.n + c.bn - 1) / c.bn), steps = (a.k + BK - 1) / BK;
-    const double alone = tiles / a.cus, rounds = alone / c.places;
-    if (rounds >= 1.0) return rounds * (c.begin + steps * c.full);
-    const double step = alone <= 1.0 && (c.places > 1 || alone <= 0.5) ? c.one : c.one + (c.full - c.one) * rounds;
-    return c.begin + steps * step;
+double tile_time(const GemmI8Args& a, const TileCost& c, double met) {
+    const double rt = a.offsets ? std::max(met, (double)a.rows / c.bm + met * c.part) : (double)((a.rows + c.bm - 1) / c.bm);
+    const double alone = rt * (double)((a.n + c.bn - 1) / c.bn) / a.cus, rounds = alone / c.places;
+    const double steps = (a.k + BK - 1) / BK, look = a.offsets ? c.grouped : 0.0;
+    if (rounds >= 1.0) {
+        const double more = c.last * (std::ceil(rounds) - rounds) / (a.offsets ? std::floor(rounds) : 1.0);
+        return look + (rounds + more) * (c.begin + steps * c.full);
+    }
+    const double shared = c.places == 1 ? rounds : std::max(0.0, (alone - 1.0) / (c.places - 1));
+    return look + c.begin + steps * (c.one + (c.full - c.one) * shared);
 }
 
 template <bool GLU>
@@ -738,24 +802,41 @@ hipError_t launch_few(const GemmI8Args& a, double per, hipStream_t st) {
 
 template <bool GLU>
 hipError_t launch_plan(const GemmI8Args& a, hipStream_t st) {
-    const double per = (double)a.rows / std::max(1, a.offsets ? a.experts : 1);
-    // Few rows for each matrix: bound by its bytes, the kernel without LDS stages.
-    // Grouped, up to where tiles of 128 are as fast (128 experts, gated: 8 rows
-    // each; plain: 6).  One matrix: while its blocks do not fill the device twice.
-    const int64_t blocks = (a.rows + 31) / 32;
-    const bool few = a.offsets ? per <= (GLU ? 9.0 : 6.0)
-                               : a.rows <= 48 || (a.rows <= 128 && blocks * a.n <= 64 * (int64_t)a.cus);
-    if (few) return launch_few<GLU>(a, per, st);
+    const double size = (double)a.n * a.k;
+    if (a.offsets) {
+        // A row or a few for each expert: bound by the weights' bytes, the kernel
+        // without LDS stages, up to where tiles are as fast (128 experts, gated, 768
+        // of 2048: 4 rows each 56 us against 62, 16 each 100 against 78), and for some
+        // more where all of it is little (8 experts, 8 rows each, 512 of 1024: 5.2
+        // against 6.8).
+        const double per = (double)a.rows / a.experts, blocks = std::max((double)a.experts, a.rows / 32.0);
+        if (per <= (GLU ? 9.0 : 6.0) || (per <= 32.0 && blocks * size <= 8 << 20)) return launch_few<GLU>(a, per, st);
+    }
     // Experts that have rows: all but those that chance leaves out.
-    const double met = a.offsets ? a.experts * (1.0 - std::exp(-per)) : 1.0;
-    const double t64 = tile_time(a, GLU ? COST_64_GATED : COST_64, per, met);
-    const double t128 = tile_time(a, GLU ? COST_128_GATED : COST_128, per, met);
-    const double t256 = tile_time(a, GLU ? COST_256_GATED : COST_256, per, met);
-    if (t64 <= t128 && t64 <= t256) return launch_tile<2, 2, 1, 1, GLU, GLU ? 2 : 3>(a, st);
-    if constexpr (GLU)
-        return t128 <= t256 ? launch_tile<4, 2, 1, 1, true, 4>(a, st) : launch_tile<4, 4, 2, 1, true, 4>(a, st);
-    else
-        return t128 <= t256 ? launch_tile<2, 4, 2, 1, false, 4>(a, st) : launch_tile<4, 4, 2, 2, false, 4>(a, st);
+    const double met = a.offsets ? a.experts * (1.0 - std::exp(-(double)a.rows / a.experts)) : 1.0;
+    const double d64 = tile_time(a, GLU ? DEEP_64_GATED : DEEP_64, met);
+    const double t64 = tile_time(a, GLU ? COST_64_GATED : COST_64, met);
+    const double t128 = tile_time(a, GLU ? COST_128_GATED : COST_128, met);
+    const double t256 = tile_time(a, GLU ? COST_256_GATED : COST_256, met);
+    double best = std::min(std::min(d64, t64), std::min(t128, t256));
+    if constexpr (!GLU) best = std::min(best, tile_time(a, DEEP_128, met));
+    if (!a.offsets && a.rows <= 128) {
+        // The kernel without stages, fitted to 33 to 128 rows; always for up to 16.
+        // (64 rows, 2048 columns of 2048: 6.0 us against 8.1 in tiles; 4096 of 4096:
+        // 14.1 against 12.1.)
+        const double blocks = a.rows <= 48 ? 1.0 : (double)((a.rows + 31) / 32);
+        if (a.rows <= 16 || 3.0 + 0.8 * a.k / 1024 + 0.2e-6 * blocks * size * (GLU ? 2 : 1) < best) return launch_few<GLU>(a, 0.0, st);
+    }
+    if constexpr (GLU) {
+        if (d64 == best) return launch_tile<2, 2, 1, 1, true, 1, 3>(a, st);
+        if (t64 == best) return launch_tile<2, 2, 1, 1, true, 2>(a, st);
+        return t128 == best ? launch_tile<4, 2, 1, 1, true, 4>(a, st) : launch_tile<4, 4, 2, 1, true, 4>(a, st);
+    } else {
+        if (d64 == best) return launch_tile<2, 2, 1, 1, false, 2, 4>(a, st);
+        if (t64 == best) return launch_tile<2, 2, 1, 1, false, 3>(a, st);
+        if (t128 == best) return launch_tile<2, 4, 2, 1, false, 4>(a, st);
+        return t256 == best ? launch_tile<4, 4, 2, 2, false, 4>(a, st) : launch_tile<4, 2, 1, 1, false, 2, 3>(a, st);
+    }
 }
 
 }  // namespace
