@@ -542,18 +542,8 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
             }
     };
 
-    i32x16 acc[S][NF][MF];
-    const auto clear = [&] {
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int i = 0; i < NF; ++i)
-#pragma unroll
-                for (int j = 0; j < MF; ++j)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) acc[s][i][j][v] = 0;
-    };
-    const auto multiply = [&](const Pieces& f) {
+    using Sums = i32x16[S][NF][MF];
+    const auto multiply = [](Sums& acc, const Pieces& f) {
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -562,18 +552,17 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
                 for (int j = 0; j < MF; ++j)
                     acc[s][i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[s][i], f.x[j], acc[s][i][j], 0, 0, 0);
     };
-    Pieces even, odd;
     // Quarters of a stage: all but the last one's products.
-    const auto quarters = [&](int stage) {
+    const auto quarters = [&](Sums& acc, Pieces& even, Pieces& odd, int stage) {
         read(odd, stage, 1);
-        multiply(even);
+        multiply(acc, even);
         read(even, stage, 2);
-        multiply(odd);
+        multiply(acc, odd);
         read(odd, stage, 3);
-        multiply(even);
+        multiply(acc, even);
         __builtin_amdgcn_sched_barrier(0);
     };
-    const auto put = [&](const Tile& q, int which, unsigned char* through) {
+    const auto put = [&](const Tile& q, const Sums& acc, int which, unsigned char* through) {
         unsigned char* const mine = through + wave * OUT;
         const float* const sx = scales + which * ROWS;
         const float* const sg = sx + BM + wn * NF * 32;
@@ -594,18 +583,27 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
         offsets(cur, off);
         for (int i = 0; i < STAGES; ++i) load(off, i, i);
         older_loads_barrier<(STAGES - 1) * LOADS>();
-        clear();
+        Sums acc;
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int j = 0; j < MF; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[s][i][j][v] = 0;
         // Steps behind the last one are zeros that nothing reads.
         const auto turn = [](int stage) { return stage + 1 == STAGES ? 0 : stage + 1; };
         if (wm * MF * 32 < cur.to - cur.from) {
+            Pieces even, odd;
             read(even, 0, 0);
             for (int st = 0, stage = 0; st < steps; ++st) {
-                quarters(stage);
+                quarters(acc, even, odd, stage);
                 older_loads_barrier<(STAGES - 2) * LOADS>();
                 load(off, st + STAGES, stage);
                 stage = turn(stage);
                 read(even, stage, 0);
-                multiply(odd);
+                multiply(acc, odd);
             }
         } else {
             for (int st = 0, stage = 0; st < steps; ++st) {
@@ -616,7 +614,7 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
         }
         keep_scales(s, 0);
         loads_barrier();
-        put(cur, 0, lds);
+        put(cur, acc, 0, lds);
         return;
     }
     int stage = 0, which = 0;
@@ -632,7 +630,15 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
     }
     loads_barrier();
     for (;;) {
-        clear();
+        Sums acc;
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int j = 0; j < MF; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[s][i][j][v] = 0;
         const bool more = t + hop < count;
         Tile next{};
         int x = -1;
@@ -658,29 +664,30 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
         else
             bring_next(stage ^ 1);
         if (wm * MF * 32 < cur.to - cur.from) {
+            Pieces even, odd;
             read(even, stage, 0);
             // Behind the barrier the other stage is there, and this one is read no more.
             for (int st = 0; st + 2 < steps; ++st) {
-                quarters(stage);
+                quarters(acc, even, odd, stage);
                 loads_barrier();
                 load(off, st + 2, stage);
                 stage ^= 1;
                 read(even, stage, 0);
-                multiply(odd);
+                multiply(acc, odd);
             }
             if (steps > 1) {
-                quarters(stage);
+                quarters(acc, even, odd, stage);
                 if (tid < BM) rows_of[tid] = x;
                 loads_barrier();
                 bring_next(stage);
                 stage ^= 1;
                 read(even, stage, 0);
-                multiply(odd);
+                multiply(acc, odd);
             }
-            quarters(stage);
+            quarters(acc, even, odd, stage);
             loads_barrier();
             stage ^= 1;
-            multiply(odd);
+            multiply(acc, odd);
         } else {
             // A tile of fewer rows, none of which are this wave's: it only loads, in
             // step with the others.
@@ -699,7 +706,7 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) tile_i8_kernel(GemmI8Args a
             stage ^= 1;
         }
         if (more) keep_scales(s, which ^ 1);
-        put(cur, which, lds + (stage ^ 1) * STAGE);
+        put(cur, acc, which, lds + (stage ^ 1) * STAGE);
         if (!more) return;
         lds_barrier();  // before the next step's loads go where the sums passed
         cur = next;
@@ -754,9 +761,9 @@ struct TileCost {
 // DEEP: a step in flight for each of several stages.
 constexpr TileCost DEEP_64{64, 64, 2, 4.4, 1.1, 0.245, 0.45, 0.14, 0.83}, DEEP_128{128, 64, 1, 4.8, 0.5, 0.25, 0.35, 0.66, 0.66};
 constexpr TileCost COST_64{64, 64, 3, 3.45, 1.6, 0.5, 0.76, 0.3, 0.8}, COST_128{128, 128, 2, 4.4, 1.0, 0.74, 1.05, 0.59, 0.71};
-constexpr TileCost COST_256{256, 256, 1, 7.8, 0.0, 1.48, 1.77, 0.52, 0.6};
+constexpr TileCost COST_256{256, 256, 1, 7.4, 0.0, 1.48, 1.77, 0.52, 0.6};
 constexpr TileCost DEEP_64_GATED{64, 64, 1, 4.8, 1.2, 0.21, 0.5, 0.63, 0.66}, COST_64_GATED{64, 64, 2, 3.1, 1.9, 0.75, 0.87, 0.15, 1.2};
-constexpr TileCost COST_128_GATED{128, 64, 2, 3.6, 2.0, 0.8, 1.11, 0.15, 1.0}, COST_256_GATED{256, 128, 1, 8.1, 1.9, 0.6, 1.55, 0.38, 0.83};
+constexpr TileCost COST_128_GATED{128, 64, 2, 3.6, 2.0, 0.8, 1.11, 0.15, 1.0}, COST_256_GATED{256, 128, 1, 7.4, 1.9, 0.6, 1.55, 0.38, 0.83};
 
 double tile_time(const GemmI8Args& a, const TileCost& c, double met) {
     const double rt = a.offsets ? std::max(met, (double)a.rows / c.bm + met * c.part) : (double)((a.rows + c.bm - 1) / c.bm);
