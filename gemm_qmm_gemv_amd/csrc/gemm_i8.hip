@@ -216,20 +216,22 @@ __global__ void __launch_bounds__(64 * W) rows_i8_kernel(GemmI8Args a) {
 //
 // A tile of 256 x 256 brings 64 KB for each step and multiplies 8 million pairs
 // of codes with them; one of 128 x 128, two of which share a compute unit and
-// hide each other's ends, brings twice as much for that.  8192 cubed: 455 us =
-// 2.4 POP/s, matrix cores 78 % busy at the clock that this load leaves (a loop
+// hide each other's ends, brings twice as much for that.  8192 cubed: 442 us =
+// 2.5 POP/s, matrix cores 78 % busy at the clock that this load leaves (a loop
 // of the instruction alone, 3.6); 8192 x 16384 of 2048 in fp16 258 us = 2.1.
-// 4096 tokens, 8 of 128 experts each: gate and up (768 of 2048) 175 us, down
-// (2048 of 768, fp32) 130 us; there, what an expert's last tile lacks in rows,
-// weights that arrive only one step ahead, and tiles that do not come out even
-// for the device leave the matrix cores 36 % and 23 % busy, memory at 3.5 and 4
-// TB/s.
+// 4096 tokens, 8 of 128 experts each: gate and up (768 of 2048) 172 to 177 us,
+// down (2048 of 768, fp32) 127; there, what an expert's last tile lacks in
+// rows, weights that arrive only one step ahead, and tiles that do not come out
+// even for the device leave the matrix cores 36 % and 23 % busy, memory at 3.7
+// and 4.2 TB/s.
 //
 // What was slower: steps of 64 codes in four stages (8192 cubed, at a time when
-// this took 495 us: 523), tiles of 256 x 128 with such steps, two on a unit (593),
-// four waves of 128 x 128 (676) and eight for 256 x 256 (3 %), weights asked for
-// into the L2 a step earlier (6 %), the 16 x 16 x 64 instruction (2.3 against 3.6
-// POP/s by itself), a branch for each block of 32 rows without rows (spills).
+// this took 495 us: 523), tiles of 256 x 128 with such steps, two on a unit
+// (593), four waves of 128 x 128 (676) and eight for 256 x 256 (3 %), weights
+// asked for into the L2 a step earlier (6 %), the 16 x 16 x 64 instruction (2.3
+// against 3.6 POP/s by itself), a branch for each block of 32 rows without rows
+// (spills), higher priority for waves that multiply (1 %) or load (4 %), bands
+// of whole experts (3 %).
 constexpr int BK = 128;
 __device__ __forceinline__ int slot_of(int r, int q) { return q ^ ((r & 7) ^ ((r >> 3) & 1)); }
 
