@@ -165,11 +165,24 @@ struct Chosen {
     float w;
 };
 
-// Whether two scores in fp32 (with a bias, or sums of two) are so far apart that
-// those in 64 bits are in the same order: `near`, what the scores themselves may
-// be off by, and 2^-24 of their size for the bias and the sum, each at either side.
+// Whether two scores in fp32 (with a bias) are so far apart that those in 64 bits
+// are in the same order: `near`, what the scores themselves may be off by, and
+// 2^-24 of their size for the bias, and twice as much.
 __device__ __forceinline__ bool apart(float high, float low, float near) {
     return high - low > near + 0x1p-22f * (fabsf(high) + fabsf(low));
+}
+
+// Between what a group's score in fp32 may lie in 64 bits: `near` for the scores
+// in it, and for biases and their sum 2^-23 of the terms' size, which may be far
+// above the sum's where they cancel, and twice as much.  `lowest`: the lowest
+// term; -inf (a bias, or a NaN placed so) is that in 64 bits, too.
+struct Range {
+    float lo, hi;
+};
+__device__ __forceinline__ Range range_of(float score, float size, float lowest, float near) {
+    if (lowest == -INF) return {-INF, -INF};
+    const float off = near + 0x1p-22f * size;
+    return off < INF ? Range{score - off, score + off} : Range{-INF, INF};
 }
 
 // Of the lanes' groups of keys the `count` highest, the lower index first among
@@ -226,15 +239,14 @@ __device__ __forceinline__ void join_two(V& x, V& y) {
     y = y > b ? y : b;
 }
 
-// Keys of experts outside the top_groups best groups become taken.  v: what is
-// compared (its order is that of the keys); s: what is summed, if two are.
-// Returns whether the last group that stays and the first that does not are
-// apart, if asked.
+// Keys of experts outside the top_groups best groups become taken.  s: what is
+// summed, if two are.  Returns whether every group that stays is above every other
+// in 64 bits, too, if asked.
 template <int L, int PER, bool APART, class Key, class V>
 __device__ __forceinline__ bool keep_groups(const RouteArgs& a, Key (&key)[PER], const V (&s)[PER], int e0, int lane, float near = 0.f) {
     const int each = a.experts / a.groups;
     const V low = -(V)INF;
-    bool clear = true;
+    Range range{0.f, 0.f};  // of that score, if asked
     using Mark = std::conditional_t<sizeof(Key) == 4 && sizeof(V) == 4, int, int64_t>;
     Mark mine = taken<Mark>();  // the score of the lane's group, in the first lane of it
     int group = lane;
@@ -250,6 +262,7 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, Key (&key)[PER],
             if (wide >= 4) k = Max{}(k, lane_move<0x4E>(k));
             if (wide >= 8) k = Max{}(k, lane_move<0x141>(k));
             mine = k;
+            if constexpr (APART) range = range_of(key_value(k), fabsf(key_value(k)), key_value(k), 0.5f * near);
         } else {
             V x = low, y = low;
 #pragma unroll
@@ -260,6 +273,7 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, Key (&key)[PER],
             V sum = x + y;
             if (sum != sum) sum = low;
             mine = order_key(sum);
+            if constexpr (APART) range = range_of(sum, fabsf(x) + fabsf(y), y, near);
         }
         if (lane % wide != 0 || e0 >= a.experts) mine = taken<Mark>();
     } else {
@@ -272,7 +286,10 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, Key (&key)[PER],
                 for (int i = 0; i < PER; ++i)
                     if (e0 + i >= lo && e0 + i < hi && key[i] > k) k = key[i];
                 k = lanes<L>(k, Max{});
-                if (lane == g) mine = k;
+                if (lane == g) {
+                    mine = k;
+                    if constexpr (APART) range = range_of(key_value(k), fabsf(key_value(k)), key_value(k), 0.5f * near);
+                }
             } else {
                 V x = low, y = low;
 #pragma unroll
@@ -280,27 +297,21 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, Key (&key)[PER],
                     if (e0 + i >= lo && e0 + i < hi) TwoBest::add(x, y, s[i]);
                 const V first = lanes<L>(x, Max{});
                 const int owner = first_of<L>(x == first, lane, L);
-                V sum = first + lanes<L>(lane == owner ? y : x, Max{});
+                const V second = lanes<L>(lane == owner ? y : x, Max{});
+                V sum = first + second;
                 if (sum != sum) sum = low;
-                if (lane == g) mine = order_key(sum);
+                if (lane == g) {
+                    mine = order_key(sum);
+                    if constexpr (APART) range = range_of(sum, fabsf(first) + fabsf(second), second, near);
+                }
             }
         }
     }
     // One bit for each group that stays.
     uint64_t stay = 0;
-    float last = 0.f;
-    for (int j = 0; j < a.top_groups + (APART ? 1 : 0); ++j) {
+    const bool has = mine != taken<Mark>();
+    for (int j = 0; j < a.top_groups; ++j) {
         const Mark m = lanes<L>(mine, Max{});
-        if (m == taken<Mark>()) break;
-        if constexpr (APART) {
-            // (The order among those that stay is of no account.)
-            const float v = key_value(m);
-            if (j == a.top_groups) {
-                clear = apart(last, v, a.group_best == 2 ? 2.f * near : near);
-                break;
-            }
-            last = v;
-        }
         const int owner = first_of<L>(mine == m, lane, 0), g = first_of<L>(mine == m, group, 0);
         stay |= 1ull << g;
         if (lane == owner) mine = taken<Mark>();
@@ -310,7 +321,15 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, Key (&key)[PER],
         const int e = e0 + i;
         if (e < a.experts && !(stay >> (e / each) & 1)) key[i] = taken<Key>();
     }
-    return clear;
+    if constexpr (APART) {
+        if (a.top_groups == a.groups) return true;
+        // (The order among those that stay is of no account.  One whose score is far
+        // from the border may be uncertain by more than one that is next to it.)
+        const bool out = mine != taken<Mark>(), in = has && !out;
+        const float lowest = lanes<L>(in ? range.lo : INF, Min{}), highest = lanes<L>(out ? range.hi : -INF, Max{});
+        return near < INF && lowest > highest;  // near: NaN where the scores are
+    }
+    return true;
 }
 
 // The choice on scores in 64 bits.
