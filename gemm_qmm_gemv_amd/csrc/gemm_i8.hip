@@ -725,6 +725,9 @@ int64_t row_tiles(const GemmI8Args& a, int bm) {
     const int64_t begun = a.rows < a.experts ? a.rows : a.experts;
     return a.rows / bm + begun;
 }
+// Work-groups that a launch has at most where each has one tile (of up to 512
+// threads, which a launch counts in 31 bits).
+constexpr int64_t ONE_EACH = 0x3fffff;
 
 template <int W, int NB, int MB, bool GLU>
 hipError_t launch_rows(const GemmI8Args& a, hipStream_t st) {
@@ -738,7 +741,7 @@ template <int WM, int WN, int MF, int NF, bool GLU, int OCC, int STAGES = 2>
 hipError_t launch_tile(const GemmI8Args& a, hipStream_t st) {
     using Shape = TileShape<WM, WN, MF, NF, GLU, STAGES>;
     const int64_t tiles = row_tiles(a, Shape::BM) * ((a.n + Shape::BN - 1) / Shape::BN);
-    if (tiles > (STAGES > 2 ? 0x3fffff : 0x3fffffff)) return hipErrorInvalidConfiguration;
+    if (tiles > (STAGES > 2 ? ONE_EACH : 0x3fffffff)) return hipErrorInvalidConfiguration;
     // As many work-groups as the device holds at once, or one for each tile; the
     // same for every die.
     int64_t grid = STAGES > 2 ? tiles : (int64_t)a.cus * std::max(1, 4 * OCC / Shape::WAVES) / 8 * 8;
@@ -768,7 +771,8 @@ constexpr TileCost COST_256{256, 256, 1, 7.4, 0.0, 1.48, 1.77, 0.52, 0.6};
 constexpr TileCost DEEP_64_GATED{64, 64, 1, 4.8, 1.2, 0.21, 0.5, 0.63, 0.66}, COST_64_GATED{64, 64, 2, 3.1, 1.9, 0.75, 0.87, 0.15, 1.2};
 constexpr TileCost COST_128_GATED{128, 64, 2, 3.6, 2.0, 0.8, 1.11, 0.15, 1.0}, COST_256_GATED{256, 128, 1, 7.4, 1.9, 0.6, 1.55, 0.38, 0.83};
 
-double tile_time(const GemmI8Args& a, const TileCost& c, double met) {
+double tile_time(const GemmI8Args& a, const TileCost& c, double met, bool one_each = false) {
+    if (one_each && row_tiles(a, c.bm) * ((a.n + c.bn - 1) / c.bn) > ONE_EACH) return HUGE_VAL;
     const double rt = a.offsets ? std::max(met, (double)a.rows / c.bm + met * c.part) : (double)((a.rows + c.bm - 1) / c.bm);
     const double alone = rt * (double)((a.n + c.bn - 1) / c.bn) / a.cus, rounds = alone / c.places;
     const double steps = (a.k + BK - 1) / BK, look = a.offsets ? c.grouped : 0.0;
@@ -820,22 +824,29 @@ hipError_t launch_plan(const GemmI8Args& a, hipStream_t st) {
         // more where all of it is little (8 experts, 8 rows each, 512 of 1024: 5.2
         // against 6.8).
         const double per = (double)a.rows / a.experts, blocks = std::max((double)a.experts, a.rows / 32.0);
-        if (per <= (GLU ? 9.0 : 6.0) || (per <= 32.0 && blocks * size <= 8 << 20)) return launch_few<GLU>(a, per, st);
+        if (per <= (GLU ? 9.0 : 6.0) || (per <= 32.0 && blocks * size <= 8 << 20)) {
+            // (Tiles take what is more than one launch of it.)
+            const hipError_t e = launch_few<GLU>(a, per, st);
+            if (e != hipErrorInvalidConfiguration) return e;
+        }
     }
     // Experts that have rows: all but those that chance leaves out.
     const double met = a.offsets ? a.experts * (1.0 - std::exp(-(double)a.rows / a.experts)) : 1.0;
-    const double d64 = tile_time(a, GLU ? DEEP_64_GATED : DEEP_64, met);
+    const double d64 = tile_time(a, GLU ? DEEP_64_GATED : DEEP_64, met, true);
     const double t64 = tile_time(a, GLU ? COST_64_GATED : COST_64, met);
     const double t128 = tile_time(a, GLU ? COST_128_GATED : COST_128, met);
     const double t256 = tile_time(a, GLU ? COST_256_GATED : COST_256, met);
     double best = std::min(std::min(d64, t64), std::min(t128, t256));
-    if constexpr (!GLU) best = std::min(best, tile_time(a, DEEP_128, met));
+    if constexpr (!GLU) best = std::min(best, tile_time(a, DEEP_128, met, true));
     if (!a.offsets && a.rows <= 128) {
         // The kernel without stages, fitted to 33 to 128 rows; always for up to 16.
         // (64 rows, 2048 columns of 2048: 6.0 us against 8.1 in tiles; 4096 of 4096:
         // 14.1 against 12.1.)
         const double blocks = a.rows <= 48 ? 1.0 : (double)((a.rows + 31) / 32);
-        if (a.rows <= 16 || 3.0 + 0.8 * a.k / 1024 + 0.2e-6 * blocks * size * (GLU ? 2 : 1) < best) return launch_few<GLU>(a, 0.0, st);
+        if (a.rows <= 16 || 3.0 + 0.8 * a.k / 1024 + 0.2e-6 * blocks * size * (GLU ? 2 : 1) < best) {
+            const hipError_t e = launch_few<GLU>(a, 0.0, st);
+            if (e != hipErrorInvalidConfiguration) return e;
+        }
     }
     if constexpr (GLU) {
         if (d64 == best) return launch_tile<2, 2, 1, 1, true, 1, 3>(a, st);
