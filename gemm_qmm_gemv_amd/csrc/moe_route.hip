@@ -40,6 +40,11 @@ constexpr int PLACE = 64;
 // Rows of counts that are summed up for the second launch, if there are more
 // than CHUNKED.
 constexpr int CHUNK = 64, CHUNKED = 256;
+// Up to this many of those sums, over chunks and experts, are added up by every
+// work-group that places; more are made running ones in a launch of their own, so
+// that a token costs the same however many there are (65536 tokens of 128 experts,
+// 2048 sums: 54.7 us either way, of 256 84.6 -> 82.9; 2^20 of 1024: 5432 -> 3203).
+constexpr int RUNNING = 2048;
 
 __device__ __forceinline__ int order_key(float v) {
     const int b = __builtin_bit_cast(int, v + 0.f);  // -0 is 0
@@ -631,11 +636,36 @@ __global__ void __launch_bounds__(256) route_sums_kernel(const uint8_t* counts, 
     for (int e = tid; e < width; e += 256) sums[(int64_t)blockIdx.x * width + e] = all_of[e];
 }
 
+// Those sums to running ones, each chunk's own included: a work-group for 64
+// experts, a lane each, its 16 waves one behind the other along the chunks.
+__global__ void __launch_bounds__(1024) route_running_kernel(u32* sums, int width, int chunks) {
+    __shared__ u32 part[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = (int)blockIdx.x * 64 + lane;
+    const int per = (chunks + 15) / 16, from = wave * per, to = from + per < chunks ? from + per : chunks;
+    u32* const p = sums + e;
+    u32 sum = 0;
+    if (e < width) {
+#pragma unroll 8
+        for (int c = from; c < to; ++c) sum += p[(int64_t)c * width];
+    }
+    part[wave][lane] = sum;
+    __syncthreads();
+    if (e >= width) return;
+    sum = 0;
+    for (int w = 0; w < wave; ++w) sum += part[w][lane];
+#pragma unroll 8
+    for (int c = from; c < to; ++c) {
+        sum += p[(int64_t)c * width];
+        p[(int64_t)c * width] = sum;
+    }
+}
+
 // Last launch where several work-groups routed: each takes PLACE tokens, adds up
 // what the experts got before, and places its pairs.  Counts (`blocks` rows, of
 // `block` tokens each) are read 16 experts a thread, rows of them side by side;
-// where there are sums of CHUNK rows, those and the rows of the own chunk.
-__global__ void __launch_bounds__(256) route_place_kernel(RouteArgs a, int block, int blocks, const u32* sums) {
+// where there are sums of CHUNK rows, those (where they are running ones, of the
+// chunk before, the own and the last) and the rows of the own chunk.
+__global__ void __launch_bounds__(256) route_place_kernel(RouteArgs a, int block, int blocks, const u32* sums, bool running) {
     extern __shared__ uint64_t mask[];  // [experts], then [2][width]: rows before this work-group, all rows
     __shared__ int part[4];
     const int tid = threadIdx.x, width = (a.experts + 15) & ~15, mine = blockIdx.x * (PLACE / block);
@@ -657,7 +687,12 @@ __global__ void __launch_bounds__(256) route_place_kernel(RouteArgs a, int block
         const int own = mine / CHUNK, chunks = (blocks + CHUNK - 1) / CHUNK;
         from = own * CHUNK;
         to = from + CHUNK < blocks ? from + CHUNK : blocks;
-        for (int i = tid; i < chunks * width; i += 256) {
+        for (int e = tid; running && e < width; e += 256) {
+            const u32 n = own > 0 ? sums[(int64_t)(own - 1) * width + e] : 0;
+            atomicAdd(before + e, (int)n);
+            atomicAdd(all + e, (int)(sums[(int64_t)(chunks - 1) * width + e] - (sums[(int64_t)own * width + e] - n)));
+        }
+        for (int i = tid; !running && i < chunks * width; i += 256) {
             const int c = i / width, e = i % width, n = (int)sums[i];
             if (n == 0 || c == own) continue;
             atomicAdd(all + e, n);
@@ -743,13 +778,19 @@ hipError_t launch(const RouteArgs& a, hipStream_t st) {
     if (e != hipSuccess || !a.offsets) return e;
     const int width = (a.experts + 15) & ~15;
     u32* sums = nullptr;
+    const int chunks = (int)((blocks + CHUNK - 1) / CHUNK);
+    const bool running = chunks * width > RUNNING;
     if (blocks > CHUNKED) {
         sums = reinterpret_cast<u32*>(a.counts + count_bytes(blocks, a.experts));
-        route_sums_kernel<<<dim3((unsigned)((blocks + CHUNK - 1) / CHUNK)), dim3(256), (size_t)width * 4, st>>>(a.counts, sums, width, (int)blocks);
+        route_sums_kernel<<<dim3((unsigned)chunks), dim3(256), (size_t)width * 4, st>>>(a.counts, sums, width, (int)blocks);
         if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (running) {
+            route_running_kernel<<<dim3((unsigned)((width + 63) / 64)), dim3(1024), 0, st>>>(sums, width, chunks);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
     }
     const size_t place = (size_t)a.experts * 8 + (size_t)width * 8;
-    route_place_kernel<<<dim3((unsigned)((a.tokens + PLACE - 1) / PLACE)), dim3(256), place, st>>>(a, block, (int)blocks, sums);
+    route_place_kernel<<<dim3((unsigned)((a.tokens + PLACE - 1) / PLACE)), dim3(256), place, st>>>(a, block, (int)blocks, sums, running);
     return hipGetLastError();
 }
 
