@@ -702,23 +702,12 @@ __global__ void __launch_bounds__(256) route_place_kernel(RouteArgs a, int block
     const int pieces = width / 16, side = 256 / pieces;  // 1 to 64 pieces of a row, so 4 rows at a time at least
     const int piece = tid % pieces, row0 = tid / pieces;
     if (row0 < side) {
-        // Sums of bytes, two in a register (of at most 64 each, so 1023 rows before they are added up).
-        int rows = 0;
+        // Sums of bytes, two in a register: a thread has at most a quarter of the
+        // rows, and a row's counts are at most its tokens.
+        static_assert(CHUNK <= CHUNKED && CHUNKED / 4 * PLACE < 1 << 16, "sums in 16 bits");
         u32 sum[8], low[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] = low[j] = 0;
-        const auto hand_in = [&] {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int e = 16 * piece + 4 * (j / 2) + j % 2;
-                if (low[j] & 0xffff) atomicAdd(before + e, (int)(low[j] & 0xffff));
-                if (low[j] >> 16) atomicAdd(before + e + 2, (int)(low[j] >> 16));
-                if (sum[j] & 0xffff) atomicAdd(all + e, (int)(sum[j] & 0xffff));
-                if (sum[j] >> 16) atomicAdd(all + e + 2, (int)(sum[j] >> 16));
-                sum[j] = low[j] = 0;
-            }
-            rows = 0;
-        };
         const auto add = [&](u32x4 v, bool earlier) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -735,10 +724,16 @@ __global__ void __launch_bounds__(256) route_place_kernel(RouteArgs a, int block
             for (int i = 0; i < 4; ++i) v[i] = counts[(int64_t)(b + i * side) * pieces];
 #pragma unroll
             for (int i = 0; i < 4; ++i) add(v[i], b + i * side < mine);
-            if ((rows += 4) > 1000) hand_in();
         }
         for (; b < to; b += side) add(counts[(int64_t)b * pieces], b < mine);
-        hand_in();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = 16 * piece + 4 * (j / 2) + j % 2;
+            if (low[j] & 0xffff) atomicAdd(before + e, (int)(low[j] & 0xffff));
+            if (low[j] >> 16) atomicAdd(before + e + 2, (int)(low[j] >> 16));
+            if (sum[j] & 0xffff) atomicAdd(all + e, (int)(sum[j] & 0xffff));
+            if (sum[j] >> 16) atomicAdd(all + e + 2, (int)(sum[j] >> 16));
+        }
     }
     __syncthreads();
     const int rows = sums_before(a.experts, part, [&](int e) { return all[e]; },
