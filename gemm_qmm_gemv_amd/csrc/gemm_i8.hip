@@ -109,9 +109,9 @@ __device__ __forceinline__ void store4(const GemmI8Args& a, int64_t p, int e, in
 // Each of W waves takes its share of K of 16 NB columns and 16 MB rows, weights
 // from memory to registers in the order of the matrix instruction, and the
 // shares meet in LDS.  16 tokens, 8 of 128 experts each, gate and up (768 of
-// 2048; 193 MB of weights): 34 us = 5.6 TB/s.  Where a matrix is small the waits
+// 2048; 193 MB of weights): 34.6 us = 5.6 TB/s.  Where a matrix is small the waits
 // are what is left, for both sides and then for the other waves: one row of 2048
-// x 1024 3.3 us, 37 of 8192 x 2048 (17 MB) 7.8.
+// x 1024 3.2 us, 37 of 8192 x 2048 (17 MB) 8.1.
 template <int W, int NB, int MB, bool GLU>
 __global__ void __launch_bounds__(64 * W) rows_i8_kernel(GemmI8Args a) {
     constexpr int S = GLU ? 2 : 1;
@@ -216,11 +216,11 @@ __global__ void __launch_bounds__(64 * W) rows_i8_kernel(GemmI8Args a) {
 //
 // A tile of 256 x 256 brings 64 KB for each step and multiplies 8 million pairs
 // of codes with them; one of 128 x 128, two of which share a compute unit and
-// hide each other's ends, brings twice as much for that.  8192 cubed: 442 us =
-// 2.5 POP/s, matrix cores 78 % busy at the clock that this load leaves (a loop
-// of the instruction alone, 3.6); 8192 x 16384 of 2048 in fp16 258 us = 2.1.
-// 4096 tokens, 8 of 128 experts each: gate and up (768 of 2048) 172 to 177 us,
-// down (2048 of 768, fp32) 127; there, what an expert's last tile lacks in
+// hide each other's ends, brings twice as much for that.  8192 cubed: 442 to 446
+// us = 2.5 POP/s, matrix cores 82 % busy at the clock that this load leaves (a loop
+// of the instruction alone, 3.6); 8192 x 16384 of 2048 in fp16 254 us = 2.2.
+// 4096 tokens, 8 of 128 experts each: gate and up (768 of 2048) 169 to 184 us,
+// down (2048 of 768, fp32) 124 to 127; there, what an expert's last tile lacks in
 // rows, weights that arrive only one step ahead, and tiles that do not come out
 // even for the device leave the matrix cores 36 % and 23 % busy, memory at 3.7
 // and 4.2 TB/s.

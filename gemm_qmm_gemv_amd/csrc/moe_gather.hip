@@ -3,7 +3,7 @@
 // summed in the order of j in fp32, so results repeat bit for bit.
 //
 // Bound by memory: every row is read once, y written once (8192 tokens of 8
-// rows of 2048 in fp16, residual, 403 MB: 67 us = 6.0 TB/s; 16 tokens: 3.3 us,
+// rows of 2048 in fp16, residual, 403 MB: 67.5 us = 6.0 TB/s; 16 tokens: 3.4 us,
 // of which the launch is half).  A thread owns 16 bytes of a row (one load);
 // indices and weights are the same for a whole work-group, and the rows of up
 // to eight choices are asked for before the first is added.

@@ -15,11 +15,12 @@
 // is taken (or not there) has a key below all of them.
 //
 // Short batches are one chain of waits and lane moves: one token of 128 experts
-// 4.3 us (an empty launch: 1.6), 37 of 256 in groups with a bias 8.5 and 4.8
+// 4.2 us (an empty launch: 1.6), 37 of 256 in groups with a bias 7.8 and 4.6
 // for the placing; a choice left open costs such a call 5 us more.  Long ones
-// are bound by vector instructions (16384 tokens of 128: 10.3 us at 72 % busy,
-// 256 in groups with a bias 42 us at 84 %; 262144 of 128: 133 us, 81 %); the
-// placing waits for memory and LDS (8.9 us; 59 for the longest).
+// are bound by vector instructions (16384 tokens of 128: 10.2 us at 73 % busy,
+// 256 in groups with a bias 41 us at 87 %; 262144 of 128: 134 us, 82 %); the
+// placing waits for memory and LDS (7.6 us; for the longest 39, and 9 for the
+// sums that it reads).
 #include <algorithm>
 #include <type_traits>
 

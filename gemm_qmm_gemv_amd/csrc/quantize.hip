@@ -2,8 +2,8 @@
 //   scale = fp32(max |x| / 127),  code = round(x / scale), ties to even.
 //
 // Bound by memory, and nearly as much by the vector units (32768 rows of 768 in
-// fp16, 75 MB: 17.6 us = 4.3 TB/s, vector units 92 % busy; 8192 of 2048, 50 MB:
-// 11.8 to 14.6, 78 %; of 8192: 43 us = 4.7): what a value costs there is kept to a
+// fp16, 76 MB: 17.7 us = 4.3 TB/s, vector units 94 % busy; 8192 of 2048, 50 MB:
+// 11.6 to 14.9, 78 %; of 8192: 42 us = 4.8): what a value costs there is kept to a
 // handful of instructions.  The whole number next to x / scale
 // comes out of one fused step with 1.5 * 2^23 (its low bits are the code, two's
 // complement), and what it leaves over, x - code * scale, is exact in another: the

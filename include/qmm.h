@@ -557,7 +557,8 @@ QMM_API qmm_status qmm_quantize_rows(const void *x, int x_fp16, int64_t x_stride
 /* y[i][j] = x_scales[i] * w_scales[j] * sum_k x[i][k] * w[j][k]
  *   w int8 [n][k] with w_scales fp32 [n]; x int8 [m][k] with x_scales fp32 [m];
  *   any codes from -128 to 127.  y fp32 [m][n], or fp16 with y_fp16.
- * The sums are exact; scaling is fp32, and fp16 outputs are rounded once more.
+ * The sums are exact; scaling is fp32, by x_scales first, and fp16 outputs are
+ * rounded once more.
  * w, x and y 16-byte aligned, scales 4-byte; k a multiple of 32, at most 32768;
  * one matrix and the activation block each below 4 GiB (else
  * QMM_ERR_UNSUPPORTED).  Any m and n; y must not overlap an input.          */

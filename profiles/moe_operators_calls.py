@@ -35,6 +35,7 @@ MORE = [
     dict(name="product_middling", op="product", m=512, n=8192, k=2048, x16=True, y16=True),
     dict(name="product_down", op="product", m=2048, n=2048, k=8192, x16=True, y16=True),
     dict(name="experts_down_fp16", op="experts", glu=False, tokens=4096, experts=128, top_k=8, n=2048, k=768, x16=True, y16=True),
+    dict(name="experts_decode_down", op="experts", glu=False, tokens=16, experts=128, top_k=8, n=2048, k=768, x16=True, y16=False),
     dict(name="experts_few", op="experts", glu=True, tokens=4096, experts=8, top_k=2, n=4096, k=2048, x16=True, y16=True),
     dict(name="experts_512", op="experts", glu=True, tokens=512, experts=128, top_k=8, n=768, k=2048, x16=True, y16=True),
     dict(name="gather_fp32", op="gather", tokens=4096, top_k=8, n=2048, f16=False, residual=True, pad=0),
@@ -117,7 +118,7 @@ def read(where, times, ctimes):
             us = [(int(r["End_Timestamp"]) - int(r["Start_Timestamp"])) / 1e3 for r in rows]
             busy = counted["SQ_BUSY_CU_CYCLES"][i][j]
             kernel = rows[0]["Kernel_Name"]
-            kernel = next(k for k in ("route_place", "route_sums", "route", "quantize_rows", "quantize", "rows_i8", "tile_i8", "gather") if k in kernel)
+            kernel = next(k for k in ("route_place", "route_running", "route_sums", "route", "quantize_rows", "quantize", "rows_i8", "tile_i8", "gather") if k in kernel)
             print("| %s | %s | %.1f (%.1f) | %.1f + %.1f | %.0f %% | %.0f %% | %.2f |" % (
                 case["name"] if j == 0 else "", kernel, statistics.median(us), min(us), counted["FETCH_SIZE"][i][j] * READ / 1e6,
                 counted["WRITE_SIZE"][i][j] * 1024 / 1e6, 100 * counted["SQ_VALU_MFMA_BUSY_CYCLES"][i][j] / (4 * busy),
