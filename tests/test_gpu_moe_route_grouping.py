@@ -81,3 +81,29 @@ def test_four_times_the_tokens_take_four_times_as_long():
         print("[time] %d tokens: %.2f ms" % (tokens, took[-1]), flush=True)
         del c
     assert took[1] < 6 * took[0], took
+
+
+def test_captured_and_replayed():
+    # The sums are made running ones in place: each replay starts from its own.
+    announce("route grouping, captured")
+    a, b = Call(70001, 128, 3, True), Call(70001, 128, 3, True)
+    a()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        b()
+    stream.synchronize()
+    with torch.cuda.graph(graph):
+        qmm.qmm_moe_route(b.logits, True, 128, None, False, 1, 1, 1, 3, True, 1.0, b.keep, b.ids, b.weights, b.pair_row, b.offsets, b.token,
+                          b.weight, b.ws, b.need, 70001, 128, stream=torch.cuda.current_stream().cuda_stream)
+    for i in range(4):
+        for c in (a, b):
+            c.logits.copy_(c.logits.flip(0))
+        a()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in ("ids", "weights", "pair_row", "offsets"):
+            assert torch.equal(getattr(a, n), getattr(b, n)), (i, n)
+        rows = int(a.offsets[-1])
+        assert torch.equal(a.token[:rows], b.token[:rows]) and torch.equal(a.weight[:rows], b.weight[:rows])
